@@ -295,6 +295,113 @@ tq_status tq_decode_attention_partial(const tq_quantizer* q, const tq_kv_cache* 
 tq_status tq_merge_partials(const float* parts_dev, int n_parts, int batch, int n_q_heads,
                             void* out_dev, int out_dtype, void* stream);
 
+/* ---------------------------------------------------- around the cache: position and norm
+ * One (batch, heads, tokens, d) view of caller-owned device memory: element (b, h, t, j) at
+ * data + b * stride_b + h * stride_h + t * stride_t + j (strides in elements, each of them a
+ * multiple of 16 bytes; data 16-byte aligned). A fused projection's output is such a view as
+ * well as tq_append's contiguous k_new is. */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_h, stride_t;
+} tq_heads;
+
+/* Rotary positions. Pair i of the first rot_dim channels, i < rot_dim / 2, turns by the angle
+ * pos[axis_of_freq[i]] * inv_freq[i]:
+ *   pos_dev       int32 n_axes x batch x n_tokens: one position per axis (text: one axis;
+ *                 images and video: time, height, width)
+ *   inv_freq_dev  fp32 rot_dim / 2
+ *   axis_of_freq  host, rot_dim / 2 values in [0, n_axes); NULL = axis 0
+ *   rot_dim       0 .. d, a multiple of 8; channels from rot_dim on are not turned
+ *   interleaved   0: pair i is channels (i, i + rot_dim / 2); 1: channels (2i, 2i + 1) */
+typedef struct {
+  const int32_t* pos_dev;
+  const float* inv_freq_dev;
+  const uint8_t* axis_of_freq;
+  int32_t n_axes, rot_dim, interleaved;
+} tq_rope;
+
+/* RMS norm of every query and key head with the position rotation, in one pass; the step
+ * between the projection and tq_append / the attention calls. Per head row x of q and k:
+ *   y = x / sqrt(mean(x^2) + eps) * w    (norm != 0; w = q_weight / k_weight, NULL = ones)
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)  for the rotary pairs,
+ * in fp32 and rounded once; the angle is the exact product of the integer position and the
+ * fp32 frequency, reduced in fp64, so far positions keep their phase. dtype (TQ_F32,
+ * TQ_BF16 or TQ_F16) is that of q, k, the outputs and the weights (d elements, 16-byte
+ * aligned). n_k_heads or n_q_heads may be 0 (that side's pointers are then not read). An
+ * output may be its own input (same pointer and strides); other overlaps are not allowed.
+ * batch = 0 or n_tokens = 0 is a no-op. */
+tq_status tq_norm_rope(const tq_rope* rope, int dtype, int batch, int n_tokens, int d,
+                       int n_q_heads, tq_heads q, tq_heads q_out, const void* q_weight_dev,
+                       int n_k_heads, tq_heads k, tq_heads k_out, const void* k_weight_dev,
+                       int norm, float eps, void* stream);
+
+/* ---------------------------------------- several query tokens over the packed cache
+ * Attention of the last n_tokens tokens of every sequence (already appended) over its packed
+ * cache, any key mode, values of 2 or 4 bits: a chunk of a prompt, drafted tokens to verify,
+ * or a single token (n_tokens = 1). Query row (b, h, t) with KV head head_map[h] attends to
+ *   i < len[b] - n_tokens + t + 1   (causal = 1)      or      i < len[b]   (causal = 0)
+ * with the scores and values of tq_decode_attention; a row that attends to nothing (a sequence
+ * shorter than n_tokens) yields zeros. q and out: (batch, n_q_heads, n_tokens, d) views in
+ * q_dtype / out_dtype (TQ_F32, TQ_BF16 or TQ_F16); they must not overlap. The products run
+ * on 16-bit tensor-core operands with 32-bit sums: rotated queries, centroids, softmax weights
+ * and dequantised values are rounded to fp16 (relative 2^-11 each), the softmax statistics
+ * and outputs are held in fp32. Non-finite cached rows reach only the query rows that attend
+ * to them. n_tokens = 0 is a no-op.
+ *
+ * Workspace (this call, tq_select_blocks and tq_decode_attention_blocks): zero-filled before
+ * its first use, 16-byte aligned; every call leaves it reusable by any of the three, whatever
+ * its sizes. Calls that share one must not overlap on the GPU. After TQ_ETIMEOUT
+ * (tq_sync_status) it must be zero-filled again. */
+tq_status tq_extend_workspace_bytes(const tq_kv_cache* cache, int n_q_heads, int n_tokens,
+                                    size_t* bytes);
+tq_status tq_extend_attention(const tq_quantizer* q, const tq_kv_cache* cache, tq_heads query,
+                              int q_dtype, int n_q_heads, int n_tokens, int causal,
+                              const int32_t* head_map, float sm_scale, tq_heads out,
+                              int out_dtype, void* workspace_dev, size_t workspace_bytes,
+                              void* stream);
+
+/* --------------------------------------------- sparse decode over selected token blocks
+ * The context of a KV head in blocks of TQ_BLOCK tokens; block i holds tokens
+ * [TQ_BLOCK i, TQ_BLOCK (i + 1)). bounds_dev: fp16 (batch, n_kv_heads, n_blocks, 2, d) with
+ * n_blocks = ceil(capacity / TQ_BLOCK): per block the channelwise minimum [0] and maximum [1]
+ * of its dequantised keys in the quantizer's rotated coordinates (the codebook part
+ * n16 c[idx] / sqrt(d); grouped: the groups' coordinates side by side, as in the idx plane). */
+#define TQ_BLOCK 64
+
+/* Recompute the bounds of the blocks that hold the last n_tokens tokens of every sequence
+ * (after tq_append of n_tokens, or all of them with n_tokens = capacity). A sequence's last
+ * block covers its tokens below len[b]. Other blocks are left as they are. */
+tq_status tq_block_bounds(const tq_quantizer* q, const tq_kv_cache* cache, void* bounds_dev,
+                          int n_tokens, void* stream);
+
+/* Choose the blocks each (sequence, KV head) attends to in one decode step. query: batch x
+ * n_q_heads x d, contiguous. The score of a block is the largest value the codebook part of
+ * the score can take within its bounds, for the KV head's query head where that is largest:
+ *   max_h sum_j max((Pi q_h)_j lo_j, (Pi q_h)_j hi_j),
+ * summed in fp64 so that the choice does not depend on the order of the sums. The first n_sink and the last
+ * n_recent blocks of a sequence (n_sink + n_recent <= n_select) are always chosen, then the
+ * highest scores (equal scores: the lower block; NaN counts as the highest). blocks_dev: int32
+ * (batch, n_kv_heads, n_select), ascending, -1 behind the last one when a sequence has fewer
+ * blocks. A KV head that no query head maps to gets its sinks and recent blocks and the
+ * lowest-numbered others. */
+tq_status tq_blocks_workspace_bytes(const tq_kv_cache* cache, int n_q_heads, int n_select,
+                                    size_t* bytes);
+tq_status tq_select_blocks(const tq_quantizer* q, const tq_kv_cache* cache, const void* bounds_dev,
+                           const void* query_dev, int q_dtype, int n_q_heads,
+                           const int32_t* head_map, int n_select, int n_sink, int n_recent,
+                           int32_t* blocks_dev, void* workspace_dev, size_t workspace_bytes,
+                           void* stream);
+
+/* tq_extend_attention of one token per sequence over the listed blocks alone: blocks_dev as
+ * tq_select_blocks writes it; entries outside [0, n_blocks) are skipped, in any order, and an
+ * entry listed twice counts twice. query / out: batch x n_q_heads x d, contiguous. */
+tq_status tq_decode_attention_blocks(const tq_quantizer* q, const tq_kv_cache* cache,
+                                     const void* query_dev, int q_dtype, int n_q_heads,
+                                     const int32_t* head_map, float sm_scale,
+                                     const int32_t* blocks_dev, int n_select, void* out_dev,
+                                     int out_dtype, void* workspace_dev, size_t workspace_bytes,
+                                     void* stream);
+
 /* Wait for `stream` (cudaStream_t as void*, NULL = legacy default stream) and report whether
  * any library kernel since the previous call gave up one of its bounded device waits (an
  * mbarrier wait on a bulk copy or a tensor-core product, limit 2 s): TQ_ETIMEOUT if so (the

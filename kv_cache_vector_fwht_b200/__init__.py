@@ -32,7 +32,9 @@ EXPORTED = ["tq_build_codebook", "tq_build_codebook_host", "tq_free", "tq_key_la
             "tq_decode_attention", "tq_decode_attention_noalloc", "tq_append_decode",
             "tq_decode_attention_partial",
             "tq_merge_partials", "tq_set_decode_policy", "tq_sync_status",
-            "tq_selftest_bounded_wait", "tq_status_string", "tq_abi_version"]
+            "tq_selftest_bounded_wait", "tq_status_string", "tq_abi_version",
+            "tq_norm_rope", "tq_extend_workspace_bytes", "tq_extend_attention", "tq_block_bounds",
+            "tq_blocks_workspace_bytes", "tq_select_blocks", "tq_decode_attention_blocks"]
 
 
 class KeyLayout(ctypes.Structure):
@@ -111,6 +113,42 @@ _lib.tq_sync_status.argtypes = [c_void_p]
 _lib.tq_sync_status.restype = c_int
 _lib.tq_selftest_bounded_wait.argtypes = [ctypes.c_uint32, c_void_p]
 _lib.tq_selftest_bounded_wait.restype = c_int
+
+
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("stride_b", c_int64), ("stride_h", c_int64),
+                ("stride_t", c_int64)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("pos_dev", c_void_p), ("inv_freq_dev", c_void_p),
+                ("axis_of_freq", c_void_p), ("n_axes", c_int32), ("rot_dim", c_int32),
+                ("interleaved", c_int32)]
+
+
+_lib.tq_norm_rope.argtypes = [POINTER(Rope), c_int, c_int, c_int, c_int, c_int, Heads, Heads,
+                              c_void_p, c_int, Heads, Heads, c_void_p, c_int, c_float, c_void_p]
+_lib.tq_norm_rope.restype = c_int
+_lib.tq_extend_workspace_bytes.argtypes = [POINTER(KVCacheDesc), c_int, c_int, POINTER(c_size_t)]
+_lib.tq_extend_workspace_bytes.restype = c_int
+_lib.tq_extend_attention.argtypes = [c_void_p, POINTER(KVCacheDesc), Heads, c_int, c_int, c_int,
+                                     c_int, POINTER(c_int32), c_float, Heads, c_int, c_void_p,
+                                     c_size_t, c_void_p]
+_lib.tq_extend_attention.restype = c_int
+_lib.tq_block_bounds.argtypes = [c_void_p, POINTER(KVCacheDesc), c_void_p, c_int, c_void_p]
+_lib.tq_block_bounds.restype = c_int
+_lib.tq_blocks_workspace_bytes.argtypes = [POINTER(KVCacheDesc), c_int, c_int, POINTER(c_size_t)]
+_lib.tq_blocks_workspace_bytes.restype = c_int
+_lib.tq_select_blocks.argtypes = [c_void_p, POINTER(KVCacheDesc), c_void_p, c_void_p, c_int,
+                                  c_int, POINTER(c_int32), c_int, c_int, c_int, c_void_p,
+                                  c_void_p, c_size_t, c_void_p]
+_lib.tq_select_blocks.restype = c_int
+_lib.tq_decode_attention_blocks.argtypes = [c_void_p, POINTER(KVCacheDesc), c_void_p, c_int,
+                                            c_int, POINTER(c_int32), c_float, c_void_p, c_int,
+                                            c_void_p, c_int, c_void_p, c_size_t, c_void_p]
+_lib.tq_decode_attention_blocks.restype = c_int
 
 
 class TQError(RuntimeError):
@@ -431,3 +469,192 @@ def tq_decode_attention_noalloc(q: Quantizer, cache: KVCache, query, out=None, h
                                             _dtype_code(out) if out is not None else TQ_F32,
                                             _ptr(scores), sld, _stream(stream)),
            "tq_decode_attention_noalloc")
+
+
+# ------------------------------------------------------- position, norm, sparse and multi-token
+TQ_BLOCK = 64   # tokens of a block that has bounds
+
+
+def _require(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_current_device(where: str, *tensors) -> None:
+    """Launches go to the current device; a tensor of another one is refused."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None:
+            _require(t.is_cuda and t.device.index == cur,
+                     f"{where}: tensors must be on the current CUDA device ({cur}), got {t.device}")
+
+
+def _heads(x) -> Heads:
+    """A (batch, heads, tokens, d) tensor with unit channel stride as the C view."""
+    sb, sh, st, _ = x.stride()
+    return Heads(x.data_ptr(), sb, sh, st)
+
+
+def _head_map(head_map, n_q_heads: int, where: str):
+    if head_map is None:
+        return None
+    _require(len(head_map) == n_q_heads, f"{where}: head_map needs one entry per query head")
+    return (c_int32 * n_q_heads)(*[int(v) for v in head_map])
+
+
+def tq_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=None,
+                 norm: bool | None = None, eps: float = 1e-6, axis_of_freq=None,
+                 interleaved: bool = False, stream=None) -> None:
+    """RMS norm of every query and key head with the position rotation, in one pass (see tq.h).
+
+    q, k, q_out, k_out: (batch, heads, n_tokens, 128) fp32 / bf16 / fp16 tensors of one type,
+    any strides with unit channel stride (views of a fused projection, tq_append's k_new); an
+    output may be its input. k and k_out may be None (queries only), and so may q and q_out.
+    positions: int32 (batch, n_tokens) or (n_axes, batch, n_tokens), contiguous. inv_freq:
+    fp32, rot_dim / 2 entries on the device. axis_of_freq: the axis each of them reads (host
+    sequence; None: axis 0). q_weight / k_weight: 128 norm weights each, in the tensors' type. norm:
+    whether to normalise; None: if a weight is given."""
+    x = q if q is not None else k
+    _require(x is not None, "tq_norm_rope: q or k is needed")
+    batch, n_tokens = x.shape[0], x.shape[2]
+    none = Heads(None, 0, 0, 0)
+    args = []
+    for a, o, w in ((q, q_out, q_weight), (k, k_out, k_weight)):
+        if a is None:
+            _require(o is None, "tq_norm_rope: an output without its input")
+            args.append((0, none, none, None))
+            continue
+        _require(o is not None and o.shape == a.shape, "tq_norm_rope: an output has its input's shape")
+        _require(a.dim() == 4 and a.shape[3] == D and a.shape[0] == batch and a.shape[2] == n_tokens,
+                 "tq_norm_rope: tensors are (batch, heads, n_tokens, 128)")
+        _require(a.stride(3) == 1 and o.stride(3) == 1, "tq_norm_rope: channels must be adjacent")
+        _require(a.dtype == x.dtype and o.dtype == x.dtype, "tq_norm_rope: one type for all tensors")
+        _require(w is None or (w.dtype == x.dtype and w.shape == (D,) and w.is_contiguous()),
+                 "tq_norm_rope: weights are 128 contiguous values of the tensors' type")
+        args.append((a.shape[1], _heads(a), _heads(o), _ptr(w)))
+    _require(positions.dtype.is_signed and positions.element_size() == 4 and not positions.is_floating_point()
+             and positions.is_contiguous() and tuple(positions.shape[-2:]) == (batch, n_tokens)
+             and positions.dim() in (2, 3),
+             "tq_norm_rope: positions are int32 (n_axes, batch, n_tokens), contiguous")
+    _require(inv_freq.dim() == 1 and inv_freq.is_contiguous() and _dtype_code(inv_freq) == TQ_F32,
+             "tq_norm_rope: inv_freq is a contiguous fp32 vector")
+    _on_current_device("tq_norm_rope", q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq)
+    pairs = inv_freq.shape[0]
+    axes = None
+    if axis_of_freq is not None:
+        _require(len(axis_of_freq) == pairs, "tq_norm_rope: one axis per frequency")
+        axes = bytes(axis_of_freq)
+    rope = Rope(_ptr(positions), _ptr(inv_freq), ctypes.cast(axes, c_void_p) if axes else None,
+                positions.shape[0] if positions.dim() == 3 else 1, 2 * pairs, int(interleaved))
+    if norm is None:
+        norm = q_weight is not None or k_weight is not None
+    (nq, qi, qo, wq), (nk, ki, ko, wk) = args
+    _check(_lib.tq_norm_rope(ctypes.byref(rope), _dtype_code(x), batch, n_tokens, D, nq, qi, qo, wq,
+                             nk, ki, ko, wk, int(norm), eps, _stream(stream)), "tq_norm_rope")
+
+
+def tq_extend_workspace_bytes(cache: KVCache, n_q_heads: int, n_tokens: int) -> int:
+    n = c_size_t()
+    _check(_lib.tq_extend_workspace_bytes(ctypes.byref(cache.desc), n_q_heads, n_tokens,
+                                          ctypes.byref(n)), "tq_extend_workspace_bytes")
+    return n.value
+
+
+def alloc_extend_workspace(cache: KVCache, n_q_heads: int, n_tokens: int, device="cuda"):
+    import torch
+    return torch.zeros(tq_extend_workspace_bytes(cache, n_q_heads, n_tokens), dtype=torch.uint8,
+                       device=device)
+
+
+def tq_extend_attention(q: Quantizer, cache: KVCache, query, out, workspace, causal: bool = True,
+                        head_map=None, sm_scale: float = 0.0, stream=None) -> None:
+    """Attention of the last n_tokens tokens of every sequence over its packed cache (see tq.h).
+    query, out: (batch, n_q_heads, n_tokens, 128) fp32 / bf16 / fp16, any strides with unit
+    channel stride; the tokens' keys and values have been appended."""
+    where = "tq_extend_attention"
+    _require(query.dim() == 4 and query.shape[0] == cache.batch and query.shape[3] == D,
+             f"{where}: query is (batch, n_q_heads, n_tokens, 128)")
+    _require(out.shape == query.shape, f"{where}: out has query's shape")
+    _require(query.stride(3) == 1 and out.stride(3) == 1, f"{where}: channels must be adjacent")
+    _on_current_device(where, query, out, workspace, cache.k_idx)
+    _check(_lib.tq_extend_attention(q.handle, ctypes.byref(cache.desc), _heads(query),
+                                    _dtype_code(query), query.shape[1], query.shape[2], int(causal),
+                                    _head_map(head_map, query.shape[1], where), sm_scale, _heads(out),
+                                    _dtype_code(out), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)), where)
+
+
+def alloc_block_bounds(cache: KVCache, device="cuda"):
+    """Bounds of every block of a cache, empty: (batch, n_kv_heads, n_blocks, 2, 128) fp16."""
+    import torch
+    return torch.zeros((cache.batch, cache.n_kv_heads, -(-cache.capacity // TQ_BLOCK), 2, D),
+                       dtype=torch.float16, device=device)
+
+
+def _check_bounds(cache: KVCache, bounds, where: str) -> None:
+    _require(tuple(bounds.shape) == (cache.batch, cache.n_kv_heads, -(-cache.capacity // TQ_BLOCK), 2, D)
+             and _dtype_code(bounds) == TQ_F16 and bounds.is_contiguous(),
+             f"{where}: bounds are what alloc_block_bounds gives for this cache")
+
+
+def tq_block_bounds(q: Quantizer, cache: KVCache, bounds, n_tokens: int, stream=None) -> None:
+    """Recompute the bounds of the blocks that hold the last n_tokens tokens of every sequence."""
+    _check_bounds(cache, bounds, "tq_block_bounds")
+    _on_current_device("tq_block_bounds", bounds, cache.k_idx)
+    _check(_lib.tq_block_bounds(q.handle, ctypes.byref(cache.desc), _ptr(bounds), n_tokens,
+                                _stream(stream)), "tq_block_bounds")
+
+
+def tq_blocks_workspace_bytes(cache: KVCache, n_q_heads: int, n_select: int) -> int:
+    n = c_size_t()
+    _check(_lib.tq_blocks_workspace_bytes(ctypes.byref(cache.desc), n_q_heads, n_select,
+                                          ctypes.byref(n)), "tq_blocks_workspace_bytes")
+    return n.value
+
+
+def alloc_blocks_workspace(cache: KVCache, n_q_heads: int, n_select: int, device="cuda"):
+    """One workspace for tq_select_blocks and tq_decode_attention_blocks."""
+    import torch
+    return torch.zeros(tq_blocks_workspace_bytes(cache, n_q_heads, n_select), dtype=torch.uint8,
+                       device=device)
+
+
+def _check_step(cache: KVCache, query, blocks, where: str) -> None:
+    _require(query.dim() == 3 and query.shape[0] == cache.batch and query.shape[2] == D and query.is_contiguous(),
+             f"{where}: query is a contiguous (batch, n_q_heads, 128)")
+    _require(blocks.dim() == 3 and tuple(blocks.shape[:2]) == (cache.batch, cache.n_kv_heads)
+             and blocks.is_contiguous() and blocks.element_size() == 4 and not blocks.is_floating_point(),
+             f"{where}: blocks is a contiguous int32 (batch, n_kv_heads, n_select)")
+
+
+def tq_select_blocks(q: Quantizer, cache: KVCache, bounds, query, blocks, workspace,
+                     n_sink: int = 1, n_recent: int = 1, head_map=None, stream=None) -> None:
+    """Choose the blocks.shape[2] blocks each (sequence, KV head) attends to (see tq.h). query:
+    (batch, n_q_heads, 128); blocks: int32 (batch, n_kv_heads, n_select) receives them, ascending
+    and -1 behind the last."""
+    where = "tq_select_blocks"
+    _check_bounds(cache, bounds, where)
+    _check_step(cache, query, blocks, where)
+    _on_current_device(where, bounds, query, blocks, workspace, cache.k_idx)
+    _check(_lib.tq_select_blocks(q.handle, ctypes.byref(cache.desc), _ptr(bounds), _ptr(query),
+                                 _dtype_code(query), query.shape[1],
+                                 _head_map(head_map, query.shape[1], where), blocks.shape[2], n_sink,
+                                 n_recent, _ptr(blocks), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)), where)
+
+
+def tq_decode_attention_blocks(q: Quantizer, cache: KVCache, query, blocks, out, workspace,
+                               head_map=None, sm_scale: float = 0.0, stream=None) -> None:
+    """One query token per sequence over the listed blocks alone (see tq.h). query, out: (batch,
+    n_q_heads, 128) fp32 / bf16 / fp16, contiguous; blocks as tq_select_blocks writes them."""
+    where = "tq_decode_attention_blocks"
+    _check_step(cache, query, blocks, where)
+    _require(out.shape == query.shape and out.is_contiguous(), f"{where}: out has query's shape, contiguous")
+    _on_current_device(where, query, blocks, out, workspace, cache.k_idx)
+    _check(_lib.tq_decode_attention_blocks(q.handle, ctypes.byref(cache.desc), _ptr(query),
+                                           _dtype_code(query), query.shape[1],
+                                           _head_map(head_map, query.shape[1], where), sm_scale,
+                                           _ptr(blocks), blocks.shape[2], _ptr(out), _dtype_code(out),
+                                           _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                           _stream(stream)), where)

@@ -1,0 +1,430 @@
+// Block bounds of the packed keys and the choice of blocks for a sparse decode step
+// (tq_block_bounds, tq_select_blocks).
+#include <cmath>
+
+#include "packed.cuh"
+
+namespace tq {
+namespace {
+
+// ------------------------------------------------------------------------------- bounds
+// min and max over a block's tokens of n16 c[idx_j] / sqrt(d), channel by channel. One block of
+// threads per token block; thread = (word of the row, every G-th token): it unpacks its index
+// words to fp16 pairs, scales them by the token's norm and keeps the pairs' minimum and maximum
+// in registers, then the G threads of a word are joined through shared memory. Levels, norms and
+// products in fp16: the result is stored in fp16 (relative 2^-11 for the level and for the
+// product, monotone in the norm, so the order of the candidates is kept up to that rounding).
+// Reads of a row are contiguous over the threads; the work is bound by HBM for long ranges.
+constexpr int kBT = 128;
+
+struct BoundsArgs {
+  const uint8_t* idx;
+  const uint16_t* norms;
+  const int32_t* len;
+  __half* bounds;
+  const DevTables* tab;
+  int n_kv_heads, capacity, n_tokens, n_blocks;
+  int row_words, n_norms;
+  int bits0, words0;     // the first channel group's code bits and index words (grouped: outliers)
+  int bits1;             // the second group's code bits (0: none)
+  float scale0, scale1;  // 1 / sqrt(channels of the group)
+};
+
+template <int BITS>
+__device__ __forceinline__ void bounds_of_word(const BoundsArgs& a, const uint32_t* words, const uint16_t* norms,
+                                               int first, int step, int n, const Levels& lv, __half2* mn, __half2* mx,
+                                               int pair0) {
+  constexpr int NP = level_pairs(BITS);
+  __half2 lo[NP], hi[NP];
+  const __half2 pinf = __half2half2(__ushort_as_half(0x7c00)), ninf = __half2half2(__ushort_as_half(0xfc00));
+#pragma unroll
+  for (int i = 0; i < NP; ++i) { lo[i] = pinf; hi[i] = ninf; }
+  constexpr int U = 4;   // rows in flight
+  for (int r0 = first; r0 < n; r0 += U * step) {
+    uint32_t w[U];
+    uint16_t nr[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = min(r0 + u * step, n - 1);   // a row seen twice changes no minimum
+      w[u] = __ldg(words + static_cast<int64_t>(r) * a.row_words);
+      nr[u] = __ldg(norms + r * a.n_norms);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t y[NP];
+      unpack_levels<BITS>(w[u], lv, y);
+      const __half2 nn = __half2half2(__ushort_as_half(nr[u]));
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&y[i]), nn);
+        lo[i] = __hmin2(lo[i], v);
+        hi[i] = __hmax2(hi[i], v);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    mn[pair0 + i] = lo[i];
+    mx[pair0 + i] = hi[i];
+  }
+}
+
+__global__ void __launch_bounds__(kBT) k_block_bounds(const __grid_constant__ BoundsArgs a) {
+  __shared__ __half2 mn[kBT / 4][kD / 2], mx[kBT / 4][kD / 2];
+  __shared__ __half res[2][kD];
+  const int b = blockIdx.z, kv = blockIdx.y;
+  const int len = min(a.len[b], a.capacity);
+  const int blk = max(0, len - a.n_tokens) / TQ_BLOCK + blockIdx.x;
+  const int n = min(TQ_BLOCK, len - blk * TQ_BLOCK);
+  if (n <= 0) return;
+  const int64_t row0 = (static_cast<int64_t>(b) * a.n_kv_heads + kv) * a.capacity + static_cast<int64_t>(blk) * TQ_BLOCK;
+  const int groups = kBT / a.row_words;
+  const int word = threadIdx.x % a.row_words, g = threadIdx.x / a.row_words;
+  const int used = min(groups, n);   // threads of a word that have a token
+  if (g < used) {
+    const bool second = a.bits1 != 0 && word >= a.words0;
+    const int bits = second ? a.bits1 : a.bits0;
+    const Levels lv = make_levels(a.tab->cent[second], bits, second ? a.scale1 : a.scale0);
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(a.idx) + row0 * a.row_words + word;
+    const uint16_t* norms = a.norms + row0 * a.n_norms + second;
+    const int pair0 = second ? level_pairs(a.bits0) * a.words0 + (word - a.words0) * level_pairs(bits) : word * level_pairs(bits);
+    switch (bits) {
+      case 1: bounds_of_word<1>(a, words, norms, g, used, n, lv, mn[g], mx[g], pair0); break;
+      case 2: bounds_of_word<2>(a, words, norms, g, used, n, lv, mn[g], mx[g], pair0); break;
+      case 3: bounds_of_word<3>(a, words, norms, g, used, n, lv, mn[g], mx[g], pair0); break;
+      default: bounds_of_word<4>(a, words, norms, g, used, n, lv, mn[g], mx[g], pair0); break;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < kD) {
+    const int p = threadIdx.x & 63, which = threadIdx.x >> 6;
+    __half2 v = which ? mx[0][p] : mn[0][p];
+    for (int i = 1; i < used; ++i) v = which ? __hmax2(v, mx[i][p]) : __hmin2(v, mn[i][p]);
+    const int pairs0 = level_pairs(a.bits0) * a.words0;
+    const bool second = p >= pairs0;
+    const int bits = second ? a.bits1 : a.bits0, q = second ? p - pairs0 : p, c0 = second ? 2 * pairs0 : 0;
+    res[which][c0 + level_channel(bits, q, 0)] = __low2half(v);
+    res[which][c0 + level_channel(bits, q, 1)] = __high2half(v);
+  }
+  __syncthreads();
+  __half2* out = reinterpret_cast<__half2*>(
+      a.bounds + ((static_cast<int64_t>(b) * a.n_kv_heads + kv) * a.n_blocks + blk) * 2 * kD);
+  out[threadIdx.x] = reinterpret_cast<const __half2*>(&res[0][0])[threadIdx.x];
+}
+
+// ------------------------------------------------------------------------------- selection
+// Scores: sum_j max(q_j lo_j, q_j hi_j) = sum_j (q_j (lo_j + hi_j) + |q_j| (hi_j - lo_j)) / 2. q = H (s . q)
+// (no 1/sqrt(d): it is the same for every block), all of it in fp64: the operands are exact
+// there and the sums are off by 2^-53, so the choice of blocks does not hang on the order of
+// a sum, at 1/2 of the fp32 rate for a few million products. A warp holds 4 channels per lane
+// of kHG rotated heads in registers and walks its blocks; the bounds are read once, 16 bytes
+// a lane. The last block of threads of a (sequence, KV head) to finish picks the blocks:
+// the n-th largest key is found by histograms of 1024 equal key ranges, each pass inside the
+// range that holds it (1-3 passes for keys that differ), and the chosen blocks are written in
+// ascending order by one prefix sum.
+constexpr int kST = 256, kSW = kST / 32;
+constexpr int kHG = 4;       // heads scored at a time
+constexpr int kHS = 16;      // rotated heads held in shared memory
+constexpr int kBPW = 8;      // blocks a warp scores
+constexpr int kBins = 1024;
+constexpr unsigned long long kAlways = ~0ull;
+
+struct SelectArgs {
+  const __half* bounds;
+  const void* q;
+  const int32_t* len;
+  const DevTables* tab;
+  int32_t* ids;
+  unsigned long long* keys;   // (batch, KV head, n_blocks)
+  int* counters;
+  int n_kv_heads, capacity, n_q_heads, n_blocks, n_select, n_sink, n_recent;
+  int q_dtype, grouped;
+  HeadLists heads;
+};
+
+__device__ __forceinline__ double shfl_xor_d(double v, int m) { return __shfl_xor_sync(kFull, v, m); }
+
+// Rotated query row (unnormalised, fp64): lane l holds coordinates 4l .. 4l + 3.
+__device__ __forceinline__ void rotate_row_f64(const SelectArgs& a, int64_t row, int lane, double (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = 4 * lane + i;
+    const int c = a.grouped ? a.tab->chan[j] : j;
+    const float x = load_element(a.q, a.q_dtype, row * kD + c);
+    v[i] = (a.tab->sign_bits[j >> 5] >> (j & 31)) & 1u ? -static_cast<double>(x) : static_cast<double>(x);
+  }
+  double t0 = v[0] + v[1], t1 = v[0] - v[1], t2 = v[2] + v[3], t3 = v[2] - v[3];
+  v[0] = t0 + t2; v[2] = t0 - t2; v[1] = t1 + t3; v[3] = t1 - t3;
+  const int top = a.grouped ? 4 : 16;   // grouped: 32-point blocks
+  for (int m = 1; m <= top; m <<= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double o = shfl_xor_d(v[i], m);
+      v[i] = lane & m ? o - v[i] : v[i] + o;
+    }
+}
+
+__device__ __forceinline__ unsigned long long order_key(double s) {
+  if (isnan(s)) return kAlways - 1;   // above every number, below what is always chosen
+  const long long b = __double_as_longlong(s + 0.0);   // -0 and 0 are one value
+  return b < 0 ? ~static_cast<unsigned long long>(b) : static_cast<unsigned long long>(b) | (1ull << 63);
+}
+
+// Inclusive prefix sum over the block's threads (two-level, kSW warps).
+__device__ __forceinline__ int block_scan(int v, int* warp_sums) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (int m = 1; m < 32; m <<= 1) {
+    const int o = __shfl_up_sync(kFull, v, m);
+    if (lane >= m) v += o;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[w] = v;
+  __syncthreads();
+  for (int i = 0; i < w; ++i) v += warp_sums[i];
+  return v;
+}
+
+// The blocks of one (sequence, KV head), by all threads of the block.
+__device__ void pick_blocks(const SelectArgs& a, int pair, int nb) {
+  __shared__ unsigned hist[kBins];
+  __shared__ int sums[kSW];
+  __shared__ unsigned long long s_lo, s_hi;
+  __shared__ int s_bin, s_need;
+  const int tid = threadIdx.x;
+  int32_t* ids = a.ids + static_cast<int64_t>(pair) * a.n_select;
+  if (nb <= a.n_select) {
+    for (int i = tid; i < a.n_select; i += kST) ids[i] = i < nb ? i : -1;
+    return;
+  }
+  const unsigned long long* keys = a.keys + static_cast<int64_t>(pair) * a.n_blocks;
+  int need = a.n_select - a.n_sink - a.n_recent;   // nb > n_select: the two ranges do not meet
+  unsigned long long T = kAlways;                  // the smallest key chosen ...
+  int ties = 0;                                    // ... and how many of its equals
+  if (need > 0) {
+    unsigned long long lo = ~0ull, hi = 0;
+    for (int i = tid; i < nb; i += kST) {
+      const unsigned long long k = __ldcg(keys + i);
+      if (k != kAlways) { lo = min(lo, k); hi = max(hi, k); }
+    }
+    if (tid == 0) { s_lo = ~0ull; s_hi = 0; }
+    __syncthreads();
+    for (int m = 16; m >= 1; m >>= 1) {
+      lo = min(lo, __shfl_xor_sync(kFull, lo, m));
+      hi = max(hi, __shfl_xor_sync(kFull, hi, m));
+    }
+    if ((tid & 31) == 0) { atomicMin(&s_lo, lo); atomicMax(&s_hi, hi); }
+    __syncthreads();
+    lo = s_lo; hi = s_hi;
+    while (true) {   // at most 7 turns: each leaves at most a 2^-9 of the key range
+      const int width = 64 - __clzll(static_cast<long long>(hi - lo));
+      const int s = max(0, width - 10);
+      for (int i = tid; i < kBins; i += kST) hist[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < nb; i += kST) {
+        const unsigned long long k = __ldcg(keys + i);
+        if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> s], 1u);
+      }
+      __syncthreads();
+      // thread t sums the bins [1024 - 4t - 4, 1024 - 4t): a scan from the highest bin down
+      constexpr int per = kBins / kST;
+      int mine = 0;
+      for (int i = 0; i < per; ++i) mine += hist[kBins - 1 - (per * tid + i)];
+      const int upto = block_scan(mine, sums);
+      if (upto >= need && upto - mine < need) {
+        int above = upto - mine, bin = kBins - 1 - per * tid;
+        while (above + static_cast<int>(hist[bin]) < need) above += hist[bin--];
+        s_bin = bin;
+        s_need = need - above;
+      }
+      __syncthreads();
+      const int bin = s_bin;
+      need = s_need;
+      const int count = hist[bin];
+      const unsigned long long first = lo + (static_cast<unsigned long long>(bin) << s);
+      const unsigned long long last = first + ((1ull << s) - 1);
+      __syncthreads();
+      lo = first;
+      hi = min(hi, last);
+      if (s == 0 || count == need) {
+        T = lo;
+        ties = s == 0 ? need : nb;   // count == need: everything from lo on, its equals too
+        break;
+      }
+    }
+  }
+  // thread t decides the blocks [t per, (t + 1) per)
+  const int per = (nb + kST - 1) / kST;
+  const int i0 = min(nb, tid * per), i1 = min(nb, i0 + per);
+  int eq = 0, more = 0;
+  for (int i = i0; i < i1; ++i) {
+    const unsigned long long k = __ldcg(keys + i);
+    eq += k == T && T != kAlways;
+    more += k > T || k == kAlways;
+  }
+  const int eq_before = block_scan(eq, sums) - eq;
+  const int eq_taken = max(0, min(eq, ties - eq_before));
+  const int end = block_scan(more + eq_taken, sums);
+  int at = end - more - eq_taken, e = 0;
+  for (int i = i0; i < i1; ++i) {
+    const unsigned long long k = __ldcg(keys + i);
+    bool take = k > T || k == kAlways;
+    if (!take && k == T) take = e++ < eq_taken;
+    if (take) ids[at++] = i;
+  }
+}
+
+__global__ void __launch_bounds__(kST) k_select_blocks(const __grid_constant__ SelectArgs a) {
+  __shared__ double qs[kHS][kD];
+  __shared__ bool last;
+  const int b = blockIdx.z, kv = blockIdx.y, pair = b * a.n_kv_heads + kv;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int len = max(0, min(a.len[b], a.capacity));
+  const int nb = (len + TQ_BLOCK - 1) / TQ_BLOCK;
+  const int h0 = a.heads.start[kv], nh = a.heads.start[kv + 1] - h0;
+  const int blk0 = (blockIdx.x * kSW + w) * kBPW;
+  if (nb > a.n_select) {   // else every block is chosen and no score is needed
+    double best[kBPW];
+#pragma unroll
+    for (int i = 0; i < kBPW; ++i) best[i] = nh ? -INFINITY : 0.0;
+    if (static_cast<int>(blockIdx.x) * kSW * kBPW < nb) {
+      for (int r0 = 0; r0 < nh; r0 += kHS) {
+        const int nr = min(kHS, nh - r0);
+        __syncthreads();
+        for (int r = w; r < (nr + kHG - 1) / kHG * kHG; r += kSW) {
+          double v[4] = {0.0, 0.0, 0.0, 0.0};
+          // heads are scored four at a time: an absent one repeats the last
+          rotate_row_f64(a, static_cast<int64_t>(b) * a.n_q_heads + a.heads.head[h0 + r0 + min(r, nr - 1)], lane, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qs[r][4 * lane + i] = v[i];
+        }
+        __syncthreads();
+        for (int g = 0; g < nr; g += kHG) {
+          double q[kHG][4];
+#pragma unroll
+          for (int h = 0; h < kHG; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[h][i] = qs[g + h][4 * lane + i];
+#pragma unroll
+          for (int i = 0; i < kBPW; ++i) {
+            const int blk = blk0 + i;
+            if (blk >= nb) break;
+            const uint2* p = reinterpret_cast<const uint2*>(a.bounds + (static_cast<int64_t>(pair) * a.n_blocks + blk) * 2 * kD) + lane;
+            const uint2 lo2 = __ldg(p), hi2 = __ldg(p + 32);
+            const float lo[4] = {half_lo(lo2.x), half_hi(lo2.x), half_lo(lo2.y), half_hi(lo2.y)};
+            const float hi[4] = {half_lo(hi2.x), half_hi(hi2.x), half_lo(hi2.y), half_hi(hi2.y)};
+            double s[kHG] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              // fp32 sums of two fp16 numbers would round: fp64 keeps them
+              const double l = lo[c], u = hi[c], mid = l + u, rad = u - l;
+#pragma unroll
+              for (int h = 0; h < kHG; ++h) s[h] = fma(q[h][c], mid, fma(fabs(q[h][c]), rad, s[h]));
+            }
+            // sums over the lanes: each exchange halves the heads a lane carries
+            const bool up = lane & 16, up2 = lane & 8;
+            double x0 = (up ? s[2] : s[0]) + shfl_xor_d(up ? s[0] : s[2], 16);
+            double x1 = (up ? s[3] : s[1]) + shfl_xor_d(up ? s[1] : s[3], 16);
+            double x = (up2 ? x1 : x0) + shfl_xor_d(up2 ? x0 : x1, 8);
+            x += shfl_xor_d(x, 4);
+            x += shfl_xor_d(x, 2);
+            x += shfl_xor_d(x, 1);
+            // the largest over the four heads; a NaN stays
+#pragma unroll
+            for (int m = 8; m <= 16; m <<= 1) {
+              const double o = shfl_xor_d(x, m);
+              x = isnan(o) || o > x ? o : x;
+            }
+            if (isnan(x) || x > best[i]) best[i] = x;
+          }
+        }
+      }
+    }
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < kBPW; ++i) {
+        const int blk = blk0 + i;
+        if (blk < nb)
+          a.keys[static_cast<int64_t>(pair) * a.n_blocks + blk] =
+              blk < a.n_sink || blk >= nb - a.n_recent ? kAlways : order_key(best[i]);
+      }
+    }
+  }
+  // the last block of threads of this (sequence, KV head) picks
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(a.counters + pair, 1) == static_cast<int>(gridDim.x) - 1;
+    if (last) a.counters[pair] = 0;
+  }
+  __syncthreads();
+  if (last) {
+    __threadfence();
+    pick_blocks(a, pair, nb);
+  }
+}
+
+}  // namespace
+
+tq_status launch_block_bounds(const tq_quantizer* q, const tq_kv_cache* c, void* bounds, int n_tokens, cudaStream_t st) {
+  BoundsArgs a;
+  a.idx = c->keys.idx;
+  a.norms = c->keys.norms;
+  a.len = c->len_dev;
+  a.bounds = static_cast<__half*>(bounds);
+  a.tab = q->dev;
+  a.n_kv_heads = c->n_kv_heads;
+  a.capacity = c->capacity;
+  a.n_tokens = n_tokens;
+  a.n_blocks = block_count(c->capacity);
+  a.row_words = q->layout.idx_bytes / 4;
+  a.n_norms = q->layout.n_norms;
+  if (q->mode == TQ_MODE_GROUPED) {
+    a.bits0 = q->bits + 1;
+    a.bits1 = q->bits;
+    a.words0 = storage_width_c(a.bits0);
+    a.scale0 = 1.f / std::sqrt(32.f);
+    a.scale1 = 1.f / std::sqrt(96.f);
+  } else {
+    a.bits0 = q->mode == TQ_MODE_PROD ? q->bits - 1 : q->bits;
+    a.bits1 = 0;
+    a.words0 = a.row_words;
+    a.scale0 = a.scale1 = 1.f / std::sqrt(static_cast<float>(kD));
+  }
+  // the blocks that n_tokens tokens can touch, wherever they begin
+  const int64_t span = (static_cast<int64_t>(n_tokens) + TQ_BLOCK - 2) / TQ_BLOCK + 1;
+  const dim3 grid(static_cast<unsigned>(span < a.n_blocks ? span : a.n_blocks), c->n_kv_heads, c->batch);
+  k_block_bounds<<<grid, kBT, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
+}
+
+size_t select_scratch_bytes(const tq_kv_cache* c) {
+  return static_cast<size_t>(c->batch) * c->n_kv_heads * block_count(c->capacity) * sizeof(unsigned long long);
+}
+
+tq_status launch_select_blocks(const tq_quantizer* q, const tq_kv_cache* c, const void* bounds, const void* query, int q_dtype,
+                               int n_q_heads, const int32_t* head_map, int n_select, int n_sink, int n_recent, int32_t* ids,
+                               void* workspace, cudaStream_t st) {
+  SelectArgs a;
+  a.bounds = static_cast<const __half*>(bounds);
+  a.q = query;
+  a.len = c->len_dev;
+  a.tab = q->dev;
+  a.ids = ids;
+  a.counters = static_cast<int*>(workspace);
+  a.keys = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
+  a.n_kv_heads = c->n_kv_heads;
+  a.capacity = c->capacity;
+  a.n_q_heads = n_q_heads;
+  a.n_blocks = block_count(c->capacity);
+  a.n_select = n_select;
+  a.n_sink = n_sink;
+  a.n_recent = n_recent;
+  a.q_dtype = q_dtype;
+  a.grouped = q->mode == TQ_MODE_GROUPED;
+  fill_head_lists(n_q_heads, c->n_kv_heads, head_map, &a.heads);
+  const dim3 grid((a.n_blocks + kSW * kBPW - 1) / (kSW * kBPW), c->n_kv_heads, c->batch);
+  k_select_blocks<<<grid, kST, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
+}
+
+}  // namespace tq

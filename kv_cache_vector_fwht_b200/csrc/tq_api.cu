@@ -7,6 +7,21 @@
 
 namespace tq {
 
+void fill_head_lists(int n_q_heads, int n_kv_heads, const int32_t* head_map, HeadLists* out) {
+  int n = 0;
+  const int per = head_map ? 0 : n_q_heads / n_kv_heads;
+  for (int kv = 0; kv < n_kv_heads; ++kv) {
+    out->start[kv] = static_cast<int16_t>(n);
+    if (head_map) {
+      for (int h = 0; h < n_q_heads; ++h)
+        if (head_map[h] == kv) out->head[n++] = static_cast<int16_t>(h);
+    } else {
+      for (int i = 0; i < per; ++i, ++n) out->head[n] = static_cast<int16_t>(n);
+    }
+  }
+  out->start[n_kv_heads] = static_cast<int16_t>(n);
+}
+
 int sm_count(int device) {
   static int cached[64] = {0};
   if (device < 0 || device >= 64) return 148;
@@ -468,6 +483,164 @@ tq_status tq_decode_attention_noalloc(const tq_quantizer* q, const tq_kv_cache* 
   if (!q->dev) return TQ_ECUDA;
   return launch_decode_noalloc(q, c, qv, q_dtype, n_q_heads, head_map, sm_scale, out, out_dtype,
                                scores, scores_ld, static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------- operators around the cache
+namespace {
+
+bool known_dtype(int dtype) { return dtype == TQ_F32 || dtype == TQ_BF16 || dtype == TQ_F16; }
+
+// A (batch, heads, tokens, d) view: base and every stride that is stepped along on 16 bytes.
+tq_status check_view(const tq_heads& x, int dtype, int batch, int n_heads, int n_tokens) {
+  if (!x.data || !aligned16(x.data)) return TQ_EINVAL;
+  const int64_t unit = 16 / elem_size(dtype);
+  if ((batch > 1 && x.stride_b % unit) || (n_heads > 1 && x.stride_h % unit) || (n_tokens > 1 && x.stride_t % unit))
+    return TQ_EINVAL;
+  return TQ_OK;
+}
+
+// The tables live on the device the quantizer was built on; launches go to the current one.
+tq_status check_device(const tq_quantizer* q) {
+  int dev = -1;
+  if (!q->dev || cudaGetDevice(&dev) != cudaSuccess) return TQ_ECUDA;
+  return dev == q->device ? TQ_OK : TQ_EINVAL;
+}
+
+tq_status check_heads(const tq_kv_cache* c, int n_q_heads, const int32_t* head_map) {
+  if (n_q_heads <= 0 || n_q_heads > kMaxHeads) return TQ_EINVAL;
+  if (c->n_kv_heads > kMaxHeads || c->batch > 65535) return TQ_EUNSUPPORTED;
+  if (head_map) {
+    for (int h = 0; h < n_q_heads; ++h)
+      if (head_map[h] < 0 || head_map[h] >= c->n_kv_heads) return TQ_EINVAL;
+  } else if (n_q_heads % c->n_kv_heads != 0) {
+    return TQ_EINVAL;
+  }
+  return TQ_OK;
+}
+
+tq_status check_space(const void* workspace, size_t have, size_t need) {
+  return !workspace || !aligned16(workspace) || have < need ? TQ_EINVAL : TQ_OK;
+}
+
+size_t blocks_workspace(const tq_kv_cache* c, int n_q_heads, int n_select) {
+  const size_t a = select_scratch_bytes(c), b = decode_blocks_scratch_bytes(c, n_q_heads, n_select);
+  return kWorkspaceHeader + (a > b ? a : b);
+}
+
+}  // namespace
+
+tq_status tq_norm_rope(const tq_rope* rope, int dtype, int batch, int n_tokens, int d, int n_q_heads, tq_heads q,
+                       tq_heads q_out, const void* q_weight, int n_k_heads, tq_heads k, tq_heads k_out,
+                       const void* k_weight, int norm, float eps, void* stream) {
+  if (!rope || batch < 0 || n_tokens < 0 || n_q_heads < 0 || n_k_heads < 0) return TQ_EINVAL;
+  if (d != kD || !known_dtype(dtype)) return TQ_EUNSUPPORTED;
+  if (rope->rot_dim < 0 || rope->rot_dim > kD || rope->rot_dim % 8) return TQ_EINVAL;
+  if (norm && !(eps >= 0.f)) return TQ_EINVAL;
+  if (rope->rot_dim > 0) {
+    if (!rope->pos_dev || !rope->inv_freq_dev || rope->n_axes < 1 || rope->n_axes > 255) return TQ_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(rope->pos_dev) & 3u) || (reinterpret_cast<uintptr_t>(rope->inv_freq_dev) & 3u))
+      return TQ_EINVAL;
+    if (rope->axis_of_freq)
+      for (int i = 0; i < rope->rot_dim / 2; ++i)
+        if (rope->axis_of_freq[i] >= rope->n_axes) return TQ_EINVAL;
+  }
+  if (batch == 0 || n_tokens == 0 || n_q_heads + static_cast<int64_t>(n_k_heads) == 0) return TQ_OK;
+  const int heads[2] = {n_q_heads, n_k_heads};
+  const tq_heads src[2] = {q, k}, dst[2] = {q_out, k_out};
+  const void* const w[2] = {q_weight, k_weight};
+  for (int s = 0; s < 2; ++s) {
+    if (heads[s] == 0) continue;
+    tq_status st = check_view(src[s], dtype, batch, heads[s], n_tokens);
+    if (st == TQ_OK) st = check_view(dst[s], dtype, batch, heads[s], n_tokens);
+    if (st != TQ_OK) return st;
+    if (w[s] && !aligned16(w[s])) return TQ_EINVAL;
+  }
+  return launch_norm_rope(rope, dtype, batch, n_tokens, heads, src, dst, w, norm, eps, static_cast<cudaStream_t>(stream));
+}
+
+tq_status tq_extend_workspace_bytes(const tq_kv_cache* c, int n_q_heads, int n_tokens, size_t* bytes) {
+  if (!c || !bytes || n_q_heads <= 0 || n_tokens < 0 || c->batch <= 0 || c->n_kv_heads <= 0 || c->capacity <= 0)
+    return TQ_EINVAL;
+  *bytes = kWorkspaceHeader + extend_scratch_bytes(c, n_q_heads, n_tokens);
+  return TQ_OK;
+}
+
+tq_status tq_extend_attention(const tq_quantizer* q, const tq_kv_cache* c, tq_heads query, int q_dtype, int n_q_heads,
+                              int n_tokens, int causal, const int32_t* head_map, float sm_scale, tq_heads out,
+                              int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q) return TQ_EINVAL;
+  tq_status st = check_cache(q, c);
+  if (st != TQ_OK) return st;
+  if ((st = check_heads(c, n_q_heads, head_map)) != TQ_OK) return st;
+  if (c->value_bits == 0 || n_tokens < 0) return TQ_EINVAL;
+  if (!known_dtype(q_dtype) || !known_dtype(out_dtype)) return TQ_EUNSUPPORTED;
+  if (n_tokens == 0) return TQ_OK;
+  if ((st = check_view(query, q_dtype, c->batch, n_q_heads, n_tokens)) != TQ_OK) return st;
+  if ((st = check_view(out, out_dtype, c->batch, n_q_heads, n_tokens)) != TQ_OK) return st;
+  if ((st = check_space(workspace, workspace_bytes, kWorkspaceHeader + extend_scratch_bytes(c, n_q_heads, n_tokens))) != TQ_OK)
+    return st;
+  if ((st = check_device(q)) != TQ_OK) return st;
+  return launch_extend(q, c, query, q_dtype, n_q_heads, n_tokens, causal, head_map, sm_scale, nullptr, 0, out, out_dtype,
+                       workspace, static_cast<cudaStream_t>(stream));
+}
+
+tq_status tq_block_bounds(const tq_quantizer* q, const tq_kv_cache* c, void* bounds, int n_tokens, void* stream) {
+  if (!q) return TQ_EINVAL;
+  tq_status st = check_cache(q, c);
+  if (st != TQ_OK) return st;
+  if (n_tokens < 0) return TQ_EINVAL;
+  if (c->n_kv_heads > 65535 || c->batch > 65535) return TQ_EUNSUPPORTED;
+  if (n_tokens == 0) return TQ_OK;
+  if (!bounds || !aligned16(bounds)) return TQ_EINVAL;
+  if ((st = check_device(q)) != TQ_OK) return st;
+  return launch_block_bounds(q, c, bounds, n_tokens, static_cast<cudaStream_t>(stream));
+}
+
+tq_status tq_blocks_workspace_bytes(const tq_kv_cache* c, int n_q_heads, int n_select, size_t* bytes) {
+  if (!c || !bytes || n_q_heads <= 0 || n_select <= 0 || c->batch <= 0 || c->n_kv_heads <= 0 || c->capacity <= 0)
+    return TQ_EINVAL;
+  *bytes = blocks_workspace(c, n_q_heads, n_select);
+  return TQ_OK;
+}
+
+tq_status tq_select_blocks(const tq_quantizer* q, const tq_kv_cache* c, const void* bounds, const void* query, int q_dtype,
+                           int n_q_heads, const int32_t* head_map, int n_select, int n_sink, int n_recent, int32_t* blocks,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q) return TQ_EINVAL;
+  tq_status st = check_cache(q, c);
+  if (st != TQ_OK) return st;
+  if ((st = check_heads(c, n_q_heads, head_map)) != TQ_OK) return st;
+  if (!known_dtype(q_dtype)) return TQ_EUNSUPPORTED;
+  if (n_select <= 0 || n_sink < 0 || n_recent < 0 || static_cast<int64_t>(n_sink) + n_recent > n_select) return TQ_EINVAL;
+  if (static_cast<int64_t>(c->batch) * c->n_kv_heads > kMaxCounters) return TQ_EUNSUPPORTED;
+  if (!bounds || !aligned16(bounds) || !query || !aligned16(query)) return TQ_EINVAL;
+  if (!blocks || (reinterpret_cast<uintptr_t>(blocks) & 3u)) return TQ_EINVAL;
+  if ((st = check_space(workspace, workspace_bytes, kWorkspaceHeader + select_scratch_bytes(c))) != TQ_OK) return st;
+  if ((st = check_device(q)) != TQ_OK) return st;
+  return launch_select_blocks(q, c, bounds, query, q_dtype, n_q_heads, head_map, n_select, n_sink, n_recent, blocks, workspace,
+                              static_cast<cudaStream_t>(stream));
+}
+
+tq_status tq_decode_attention_blocks(const tq_quantizer* q, const tq_kv_cache* c, const void* query, int q_dtype, int n_q_heads,
+                                     const int32_t* head_map, float sm_scale, const int32_t* blocks, int n_select, void* out,
+                                     int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q) return TQ_EINVAL;
+  tq_status st = check_cache(q, c);
+  if (st != TQ_OK) return st;
+  if ((st = check_heads(c, n_q_heads, head_map)) != TQ_OK) return st;
+  if (c->value_bits == 0 || n_select <= 0) return TQ_EINVAL;
+  if (!known_dtype(q_dtype) || !known_dtype(out_dtype)) return TQ_EUNSUPPORTED;
+  if (!blocks || (reinterpret_cast<uintptr_t>(blocks) & 3u)) return TQ_EINVAL;
+  const int64_t row = static_cast<int64_t>(n_q_heads) * kD;
+  const tq_heads qv{const_cast<void*>(query), row, kD, 0}, ov{out, row, kD, 0};
+  if ((st = check_view(qv, q_dtype, c->batch, n_q_heads, 1)) != TQ_OK) return st;
+  if ((st = check_view(ov, out_dtype, c->batch, n_q_heads, 1)) != TQ_OK) return st;
+  if ((st = check_space(workspace, workspace_bytes,
+                        kWorkspaceHeader + decode_blocks_scratch_bytes(c, n_q_heads, n_select))) != TQ_OK)
+    return st;
+  if ((st = check_device(q)) != TQ_OK) return st;
+  return launch_extend(q, c, qv, q_dtype, n_q_heads, 1, /*causal=*/0, head_map, sm_scale, blocks, n_select, ov, out_dtype,
+                       workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

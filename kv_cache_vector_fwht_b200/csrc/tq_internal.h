@@ -127,4 +127,35 @@ tq_status launch_decode_noalloc(const tq_quantizer* q, const tq_kv_cache* cache,
 
 int sm_count(int device);
 
+// ---------------------------------------------------- operators around the cache
+// Query heads by KV head: those of KV head kv are head[start[kv] .. start[kv + 1]).
+constexpr int kMaxHeads = 512;
+struct HeadLists {
+  int16_t head[kMaxHeads];
+  int16_t start[kMaxHeads + 1];
+};
+// head_map as in tq_decode_attention (checked by the caller); n_kv_heads <= kMaxHeads.
+void fill_head_lists(int n_q_heads, int n_kv_heads, const int32_t* head_map, HeadLists* out);
+
+// Workspace of tq_extend_attention, tq_select_blocks and tq_decode_attention_blocks: counters
+// that are zero between calls, at the same place whatever the call, then scratch.
+constexpr size_t kWorkspaceHeader = 64 << 10;
+constexpr int kMaxCounters = kWorkspaceHeader / sizeof(int);
+inline int block_count(int capacity) { return (capacity + TQ_BLOCK - 1) / TQ_BLOCK; }
+
+tq_status launch_norm_rope(const tq_rope* rope, int dtype, int batch, int n_tokens, const int (&n_heads)[2],
+                           const tq_heads (&src)[2], const tq_heads (&dst)[2], const void* const (&w)[2], int norm,
+                           float eps, cudaStream_t st);
+size_t extend_scratch_bytes(const tq_kv_cache* c, int n_q_heads, int n_tokens);
+size_t decode_blocks_scratch_bytes(const tq_kv_cache* c, int n_q_heads, int n_select);
+size_t select_scratch_bytes(const tq_kv_cache* c);
+// blocks: nullable list of n_select blocks per (sequence, KV head)
+tq_status launch_extend(const tq_quantizer* q, const tq_kv_cache* c, const tq_heads& query, int q_dtype, int n_q_heads,
+                        int n_tokens, int causal, const int32_t* head_map, float sm_scale, const int32_t* blocks,
+                        int n_select, const tq_heads& out, int out_dtype, void* workspace, cudaStream_t st);
+tq_status launch_block_bounds(const tq_quantizer* q, const tq_kv_cache* c, void* bounds, int n_tokens, cudaStream_t st);
+tq_status launch_select_blocks(const tq_quantizer* q, const tq_kv_cache* c, const void* bounds, const void* query, int q_dtype,
+                               int n_q_heads, const int32_t* head_map, int n_select, int n_sink, int n_recent, int32_t* ids,
+                               void* workspace, cudaStream_t st);
+
 }  // namespace tq
