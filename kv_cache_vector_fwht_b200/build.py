@@ -20,7 +20,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 SOURCES = ["tq_api.cu", "quantize.cu", "keys_tc.cu", "dequant.cu", "decode.cu", "decode_prod.cu",
            "decode_mse.cu", "decode_grp.cu", "append.cu", "rope.cu", "blocks.cu", "extend.cu",
            "tq_host.cpp"]
-HEADERS = ["tq_internal.h", "tq_device.cuh", "decode_kernel.cuh", "packed.cuh",
+HEADERS = ["tq_internal.h", "tq_device.cuh", "decode_kernel.cuh", "packed.cuh", "extend_kernel.cuh",
            os.path.join("..", "..", "include", "tq.h")]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3",

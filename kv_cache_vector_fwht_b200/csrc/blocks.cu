@@ -10,10 +10,9 @@ namespace {
 // ------------------------------------------------------------------------------- bounds
 // min and max over a block's tokens of n16 c[idx_j] / sqrt(d), channel by channel. One block of
 // threads per token block; thread = (word of the row, every G-th token): it unpacks its index
-// words to fp16 pairs, scales them by the token's norm and keeps the pairs' minimum and maximum
-// in registers, then the G threads of a word are joined through shared memory. Levels, norms and
-// products in fp16: the result is stored in fp16 (relative 2^-11 for the level and for the
-// product, monotone in the norm, so the order of the candidates is kept up to that rounding).
+// words to fp16 levels, scales them by the token's norm and keeps the channels' minimum and maximum
+// in registers (fp32), then the G threads of a word are joined through shared memory in fp16, the
+// type of the result: one rounding of the product.
 // Reads of a row are contiguous over the threads; the work is bound by HBM for long ranges.
 constexpr int kBT = 128;
 
@@ -27,18 +26,17 @@ struct BoundsArgs {
   int row_words, n_norms;
   int bits0, words0;     // the first channel group's code bits and index words (grouped: outliers)
   int bits1;             // the second group's code bits (0: none)
-  float scale0, scale1;  // 1 / sqrt(channels of the group)
+  float scale0, scale1;  // level scale / sqrt(channels of the group)
 };
 
 template <int BITS>
 __device__ __forceinline__ void bounds_of_word(const BoundsArgs& a, const uint32_t* words, const uint16_t* norms,
-                                               int first, int step, int n, const Levels& lv, __half2* mn, __half2* mx,
-                                               int pair0) {
+                                               int first, int step, int n, const Levels& lv, float scale, __half2* mn,
+                                               __half2* mx, int pair0) {
   constexpr int NP = level_pairs(BITS);
-  __half2 lo[NP], hi[NP];
-  const __half2 pinf = __half2half2(__ushort_as_half(0x7c00)), ninf = __half2half2(__ushort_as_half(0xfc00));
+  float lo[2 * NP], hi[2 * NP];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) { lo[i] = pinf; hi[i] = ninf; }
+  for (int i = 0; i < 2 * NP; ++i) { lo[i] = INFINITY; hi[i] = -INFINITY; }
   constexpr int U = 4;   // rows in flight
   for (int r0 = first; r0 < n; r0 += U * step) {
     uint32_t w[U];
@@ -53,19 +51,21 @@ __device__ __forceinline__ void bounds_of_word(const BoundsArgs& a, const uint32
     for (int u = 0; u < U; ++u) {
       uint32_t y[NP];
       unpack_levels<BITS>(w[u], lv, y);
-      const __half2 nn = __half2half2(__ushort_as_half(nr[u]));
+      const float f = __half2float(__ushort_as_half(nr[u])) * scale;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&y[i]), nn);
-        lo[i] = __hmin2(lo[i], v);
-        hi[i] = __hmax2(hi[i], v);
+        const float v0 = half_lo(y[i]) * f, v1 = half_hi(y[i]) * f;
+        lo[2 * i] = fminf(lo[2 * i], v0);
+        hi[2 * i] = fmaxf(hi[2 * i], v0);
+        lo[2 * i + 1] = fminf(lo[2 * i + 1], v1);
+        hi[2 * i + 1] = fmaxf(hi[2 * i + 1], v1);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    mn[pair0 + i] = lo[i];
-    mx[pair0 + i] = hi[i];
+  for (int i = 0; i < NP; ++i) {   // rounding is monotone: the minimum of the rounded is the rounded minimum
+    mn[pair0 + i] = __floats2half2_rn(lo[2 * i], lo[2 * i + 1]);
+    mx[pair0 + i] = __floats2half2_rn(hi[2 * i], hi[2 * i + 1]);
   }
 }
 
@@ -84,15 +84,16 @@ __global__ void __launch_bounds__(kBT) k_block_bounds(const __grid_constant__ Bo
   if (g < used) {
     const bool second = a.bits1 != 0 && word >= a.words0;
     const int bits = second ? a.bits1 : a.bits0;
-    const Levels lv = make_levels(a.tab->cent[second], bits, second ? a.scale1 : a.scale0);
+    const Levels lv = load_levels(a.tab, second);
+    const float scale = second ? a.scale1 : a.scale0;
     const uint32_t* words = reinterpret_cast<const uint32_t*>(a.idx) + row0 * a.row_words + word;
     const uint16_t* norms = a.norms + row0 * a.n_norms + second;
     const int pair0 = second ? level_pairs(a.bits0) * a.words0 + (word - a.words0) * level_pairs(bits) : word * level_pairs(bits);
     switch (bits) {
-      case 1: bounds_of_word<1>(a, words, norms, g, used, n, lv, mn[g], mx[g], pair0); break;
-      case 2: bounds_of_word<2>(a, words, norms, g, used, n, lv, mn[g], mx[g], pair0); break;
-      case 3: bounds_of_word<3>(a, words, norms, g, used, n, lv, mn[g], mx[g], pair0); break;
-      default: bounds_of_word<4>(a, words, norms, g, used, n, lv, mn[g], mx[g], pair0); break;
+      case 1: bounds_of_word<1>(a, words, norms, g, used, n, lv, scale, mn[g], mx[g], pair0); break;
+      case 2: bounds_of_word<2>(a, words, norms, g, used, n, lv, scale, mn[g], mx[g], pair0); break;
+      case 3: bounds_of_word<3>(a, words, norms, g, used, n, lv, scale, mn[g], mx[g], pair0); break;
+      default: bounds_of_word<4>(a, words, norms, g, used, n, lv, scale, mn[g], mx[g], pair0); break;
     }
   }
   __syncthreads();
@@ -382,13 +383,13 @@ tq_status launch_block_bounds(const tq_quantizer* q, const tq_kv_cache* c, void*
     a.bits0 = q->bits + 1;
     a.bits1 = q->bits;
     a.words0 = storage_width_c(a.bits0);
-    a.scale0 = 1.f / std::sqrt(32.f);
-    a.scale1 = 1.f / std::sqrt(96.f);
+    a.scale0 = q->lv_scale[0] / std::sqrt(32.f);
+    a.scale1 = q->lv_scale[1] / std::sqrt(96.f);
   } else {
     a.bits0 = q->mode == TQ_MODE_PROD ? q->bits - 1 : q->bits;
     a.bits1 = 0;
     a.words0 = a.row_words;
-    a.scale0 = a.scale1 = 1.f / std::sqrt(static_cast<float>(kD));
+    a.scale0 = a.scale1 = q->lv_scale[0] / std::sqrt(static_cast<float>(kD));
   }
   // the blocks that n_tokens tokens can touch, wherever they begin
   const int64_t span = (static_cast<int64_t>(n_tokens) + TQ_BLOCK - 2) / TQ_BLOCK + 1;

@@ -1,169 +1,165 @@
-// Attention of several query tokens over the packed cache, dense or over listed blocks
-// (tq_extend_attention, tq_decode_attention_blocks).
+// Multi-token and sparse attention over the packed cache, host side: the tile of query rows, the
+// split of every sequence's context over the SMs, and the launch (the kernel: extend_kernel.cuh).
+#include <algorithm>
 #include <cmath>
 
-#include "packed.cuh"
+#include "extend_kernel.cuh"
 
 namespace tq {
 namespace {
 
-constexpr int kET = 128;
+using namespace ext;
 
-struct ExtendArgs {
-  const uint8_t* k_idx;
-  const uint8_t* k_sgn;
-  const uint16_t* k_nrm;
-  const uint8_t* v_q;
-  const uint16_t* v_par;
-  const int32_t* len;
-  const int32_t* blocks;   // nullable: (batch, KV head, n_select) listed blocks
-  const DevTables* tab;
-  const void* q;
-  void* out;
-  int64_t qb, qh, qt, ob, oh, ot;
-  int q_dtype, out_dtype;
-  int n_kv_heads, capacity, n_tokens, n_select, n_blocks, causal;
-  int mode, bits, vbits, idx_bytes, n_norms;
-  float scale_log2;
-  HeadLists heads;
-};
+constexpr int kMaxSlots = 1024;     // partial records of a launch: blocks of threads that share items
+constexpr int kSmemMax = 227 * 1024;
+// A block of threads costs about this many tiles before its first and after its last one (query
+// rotation, pipeline fill, joining the streams).
+constexpr int kFixedTiles = 10;
 
-__device__ __forceinline__ int code_at(const uint8_t* row, int bits, int j) {
-  const int w = storage_width_c(bits);
-  return (row[j * w >> 3] >> (j * w & 7)) & ((1 << bits) - 1);
+int tile_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+// Upper bound of the partial records for any lengths and any head map.
+size_t scratch_bytes(const tq_kv_cache* c, int64_t most_rows, int64_t most_tiles) {
+  const int n = tile_rows(static_cast<int>(std::min<int64_t>(most_rows, 128)));
+  const int64_t items = static_cast<int64_t>(c->batch) * c->n_kv_heads * ((most_rows + n - 1) / n);
+  const int64_t slots = std::min<int64_t>(kMaxSlots, items * most_tiles);
+  return static_cast<size_t>(slots) * n * kPartFloats * sizeof(float);
 }
 
-// One block of threads per query row: thread = key for the scores of 128 keys at a time, then
-// thread = channel for their weighted values.
-__global__ void __launch_bounds__(kET) k_extend_simple(const __grid_constant__ ExtendArgs a) {
-  __shared__ float qr[kD], sq[kD], p[kET], red[kET];
-  __shared__ int rows[kET];
-  const int tid = threadIdx.x, t = blockIdx.x, b = blockIdx.z;
-  int kv = 0;
-  while (static_cast<int>(blockIdx.y) >= a.heads.start[kv + 1]) ++kv;
-  const int h = a.heads.head[blockIdx.y];
-  const int len = max(0, min(a.len[b], a.capacity));
-  const int limit = a.causal ? min(len, len - a.n_tokens + t + 1) : len;
-  const bool grp = a.mode == TQ_MODE_GROUPED;
-  // rotated query
-  {
-    const int c = grp ? a.tab->chan[tid] : tid;
-    float x = load_element(a.q, a.q_dtype, b * a.qb + h * a.qh + t * a.qt + c);
-    qr[tid] = flip_sign(x, a.tab->sign_bits[tid >> 5], tid & 31);
-    for (int m = 1; m < (grp ? 32 : kD); m <<= 1) {
-      __syncthreads();
-      const float u = qr[tid], v = qr[tid ^ m];
-      __syncthreads();
-      qr[tid] = tid & m ? v - u : u + v;
-    }
-    __syncthreads();
-    qr[tid] *= grp ? rsqrtf(32.f) : rsqrtf(128.f);
-    __syncthreads();
-    float s = 0.f;
-    if (a.mode == TQ_MODE_PROD)
-      for (int j = 0; j < kD; ++j) s = fmaf(__half2float(a.tab->s_rot_t[j * kD + tid]), qr[j], s);
-    sq[tid] = s * (1.2533141373155003f / kD);
-    __syncthreads();
-  }
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  const int64_t base = (static_cast<int64_t>(b) * a.n_kv_heads + kv) * a.capacity;
-  const int32_t* list = a.blocks ? a.blocks + (static_cast<int64_t>(b) * a.n_kv_heads + kv) * a.n_select : nullptr;
-  const int total = list ? a.n_select * TQ_BLOCK : limit;
-  for (int i0 = 0; i0 < total; i0 += kET) {
-    int i = i0 + tid;
-    if (list) {
-      const int blk = i < total ? list[i / TQ_BLOCK] : -1;
-      i = blk >= 0 && blk < a.n_blocks ? blk * TQ_BLOCK + i % TQ_BLOCK : limit;
-    }
-    const bool ok = i < limit;
-    float s = -INFINITY;
-    if (ok) {
-      const uint8_t* idx = a.k_idx + (base + i) * a.idx_bytes;
-      const float n0 = __half2float(__ushort_as_half(a.k_nrm[(base + i) * a.n_norms]));
-      if (grp) {
-        float s0 = 0.f, s1 = 0.f;
-        for (int j = 0; j < 32; ++j) s0 = fmaf(qr[j], a.tab->cent[0][code_at(idx, a.bits + 1, j)], s0);
-        const uint8_t* rest = idx + 4 * storage_width_c(a.bits + 1);
-        for (int j = 0; j < 96; ++j) s1 = fmaf(qr[32 + j], a.tab->cent[1][code_at(rest, a.bits, j)], s1);
-        s = n0 * s0 * rsqrtf(32.f) + __half2float(__ushort_as_half(a.k_nrm[(base + i) * 2 + 1])) * s1 * rsqrtf(96.f);
+struct Plan {
+  int n, row_tiles, blocks;
+};
+
+// Splits: sequence b's items (KV head x tile of query rows) get splits[b] blocks of threads each, so
+// that no block has more than T tiles; T is chosen for the fewest rounds over the SMs times (T +
+// fixed cost). The kernel divides an item's tiles by the lengths on the device: host lengths
+// only shape the split.
+Plan plan_extend(const tq_kv_cache* c, int n_tokens, int n_select, bool listed, int sms, ExtendArgs* a) {
+  Plan p;
+  int most = 0;
+  for (int kv = 0; kv < c->n_kv_heads; ++kv) most = std::max(most, a->heads.start[kv + 1] - a->heads.start[kv]);
+  const int64_t rows = static_cast<int64_t>(most) * n_tokens;
+  p.n = tile_rows(static_cast<int>(std::min<int64_t>(rows, 128)));
+  p.row_tiles = static_cast<int>((rows + p.n - 1) / p.n);
+  const int64_t items = static_cast<int64_t>(c->n_kv_heads) * p.row_tiles;
+  auto tiles_of = [&](int b) {
+    const int len = std::max(1, c->len_host[b]);
+    return listed ? (std::min(n_select, block_count(len)) + 1) / 2 : (len + kTile - 1) / kTile;
+  };
+  int longest = 1;
+  for (int b = 0; b < c->batch; ++b) longest = std::max(longest, tiles_of(b));
+  const bool one_by_one = c->batch <= kMaxList;
+  const int64_t all = items * c->batch;
+  auto splits_of = [&](int b, int T) { return ((one_by_one ? tiles_of(b) : longest) + T - 1) / T; };
+  int best_T = longest;
+  if (all <= kMaxSlots) {
+    double best = 1e300;
+    const int most_splits = static_cast<int>(std::min<int64_t>(longest, std::max<int64_t>(4, 3 * sms / all + 1)));
+    for (int s = 1; s <= most_splits; ++s) {
+      const int T = (longest + s - 1) / s;
+      int64_t blocks = 0;
+      if (one_by_one) {
+        for (int b = 0; b < c->batch; ++b) blocks += items * splits_of(b, T);
       } else {
-        const int bits = a.mode == TQ_MODE_PROD ? a.bits - 1 : a.bits;
-        float s0 = 0.f;
-        for (int j = 0; j < kD; ++j) s0 = fmaf(qr[j], a.tab->cent[0][code_at(idx, bits, j)], s0);
-        s = n0 * s0 * rsqrtf(128.f);
-        if (a.mode == TQ_MODE_PROD) {
-          float s1 = 0.f;
-          for (int j = 0; j < kD; ++j) s1 += code_at(a.k_sgn + (base + i) * (kD / 8), 1, j) ? sq[j] : -sq[j];
-          s = fmaf(__half2float(__ushort_as_half(a.k_nrm[(base + i) * 2 + 1])), s1, s);
-        }
+        blocks = all * splits_of(0, T);
       }
-      s *= a.scale_log2;
+      if (s > 1 && blocks > kMaxSlots) break;
+      const double rounds = std::ceil(static_cast<double>(blocks) / sms);
+      const double cost = rounds * (T + kFixedTiles) + (s > 1 ? 1.0 + 0.1 * s : 0.0);
+      if (cost < best) { best = cost; best_T = T; }
     }
-    red[tid] = s;
-    rows[tid] = ok ? i : -1;
-    __syncthreads();
-    float mc = m;
-    for (int k = 0; k < kET; ++k) mc = fmaxf(mc, red[k]);
-    const float ref = mc == -INFINITY ? 0.f : mc;
-    p[tid] = ok ? exp2f(s - ref) : 0.f;
-    __syncthreads();
-    const float f = exp2f(m - ref);
-    l *= f;
-    o *= f;
-    for (int k = 0; k < kET; ++k) {
-      if (rows[k] < 0) continue;
-      const int64_t r = base + rows[k];
-      const uint16_t* par = a.v_par + r * 8 + 2 * (tid >> 5);
-      const float v = fmaf(static_cast<float>(code_at(a.v_q + r * (kD * a.vbits / 8), a.vbits, tid)),
-                           __half2float(__ushort_as_half(par[1])), __half2float(__ushort_as_half(par[0])));
-      l += p[k];
-      o = fmaf(p[k], v, o);
-    }
-    m = mc;
-    __syncthreads();
   }
-  store_element(a.out, a.out_dtype, b * a.ob + h * a.oh + t * a.ot + tid, l > 0.f || isnan(l) ? o / l : 0.f);
+  a->row_tiles = p.row_tiles;
+  int64_t blocks = 0;
+  if (one_by_one) {
+    for (int b = 0; b < c->batch; ++b) {
+      a->first[b] = static_cast<int>(blocks);
+      a->splits[b] = static_cast<int16_t>(splits_of(b, best_T));
+      blocks += items * a->splits[b];
+    }
+    a->first[c->batch] = static_cast<int>(blocks);
+    a->uniform_splits = 1;
+  } else {
+    a->uniform_splits = splits_of(0, best_T);
+    blocks = all * a->uniform_splits;
+  }
+  p.blocks = blocks > 0x7fffffff ? -1 : static_cast<int>(blocks);
+  return p;
+}
+
+template <int N>
+tq_status launch_rows(ExtendArgs& a, int blocks, cudaStream_t st) {
+  const int fixed = smem_fixed(N, a.mode == TQ_MODE_PROD ? 2 * kD : kD);
+  a.stages = std::min(kMaxStages, (kSmemMax - fixed) / a.stage_bytes);
+  const int smem = fixed + a.stages * a.stage_bytes;
+  if (cudaFuncSetAttribute(k_extend<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
+    return TQ_ECUDA;
+  k_extend<N><<<blocks, kThreads, smem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
 }
 
 }  // namespace
 
-size_t extend_scratch_bytes(const tq_kv_cache*, int, int) { return 0; }
-size_t decode_blocks_scratch_bytes(const tq_kv_cache*, int, int) { return 0; }
+size_t extend_scratch_bytes(const tq_kv_cache* c, int n_q_heads, int n_tokens) {
+  return scratch_bytes(c, static_cast<int64_t>(n_q_heads) * n_tokens, (c->capacity + kTile - 1) / kTile);
+}
+size_t decode_blocks_scratch_bytes(const tq_kv_cache* c, int n_q_heads, int n_select) {
+  return scratch_bytes(c, n_q_heads, (n_select + 1) / 2);
+}
 
 tq_status launch_extend(const tq_quantizer* q, const tq_kv_cache* c, const tq_heads& query, int q_dtype, int n_q_heads,
                         int n_tokens, int causal, const int32_t* head_map, float sm_scale, const int32_t* blocks,
-                        int n_select, const tq_heads& out, int out_dtype, void*, cudaStream_t st) {
-  ExtendArgs a;
+                        int n_select, const tq_heads& out, int out_dtype, void* workspace, cudaStream_t st) {
+  static thread_local ExtendArgs a;
   a.k_idx = c->keys.idx;
   a.k_sgn = c->keys.signs;
-  a.k_nrm = c->keys.norms;
+  a.k_nrm = reinterpret_cast<const uint8_t*>(c->keys.norms);
   a.v_q = c->values.q;
-  a.v_par = c->values.params;
+  a.v_par = reinterpret_cast<const uint8_t*>(c->values.params);
   a.len = c->len_dev;
   a.blocks = blocks;
   a.tab = q->dev;
   a.q = query.data;
   a.out = out.data;
+  a.counters = static_cast<int*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
+  a.err = device_error_word();
   a.qb = query.stride_b; a.qh = query.stride_h; a.qt = query.stride_t;
   a.ob = out.stride_b; a.oh = out.stride_h; a.ot = out.stride_t;
   a.q_dtype = q_dtype;
   a.out_dtype = out_dtype;
+  a.batch = c->batch;
   a.n_kv_heads = c->n_kv_heads;
   a.capacity = c->capacity;
   a.n_tokens = n_tokens;
   a.n_select = n_select;
   a.n_blocks = block_count(c->capacity);
-  a.causal = causal;
+  a.causal = causal != 0;
   a.mode = q->mode;
-  a.bits = q->bits;
-  a.vbits = c->value_bits;
+  a.bits0 = q->mode == TQ_MODE_PROD ? q->bits - 1 : q->mode == TQ_MODE_GROUPED ? q->bits + 1 : q->bits;
+  a.bits1 = q->bits;
   a.idx_bytes = q->layout.idx_bytes;
-  a.n_norms = q->layout.n_norms;
+  a.sgn_bytes = q->layout.sign_bytes;
+  a.nrm_bytes = 2 * q->layout.n_norms;
+  a.vbits = c->value_bits;
+  a.vq_bytes = kD * c->value_bits / 8;
+  a.stage_bytes = kTile * (a.idx_bytes + a.sgn_bytes + a.nrm_bytes + a.vq_bytes + 16);
+  const float ch0 = q->mode == TQ_MODE_GROUPED ? 32.f : 128.f;
+  a.key_scale0 = q->lv_scale[0] / std::sqrt(ch0);
+  a.key_scale1 = q->lv_scale[1] / std::sqrt(96.f);
+  // rho = r16 / n16 sqrt(pi/2) / d over the level side's factor and the sketch rows' 1/8
+  a.sketch_ratio = 1.2533141373155003f / kD * 8.f / a.key_scale0;
   const float scale = sm_scale > 0.f ? sm_scale : 1.f / std::sqrt(static_cast<float>(kD));
   a.scale_log2 = scale * 1.4426950408889634074f;
   fill_head_lists(n_q_heads, c->n_kv_heads, head_map, &a.heads);
-  k_extend_simple<<<dim3(n_tokens, n_q_heads, c->batch), kET, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
+  const Plan p = plan_extend(c, n_tokens, n_select, blocks != nullptr, std::max(1, sm_count(q->device)), &a);
+  if (p.blocks < 0) return TQ_EUNSUPPORTED;
+  switch (p.n) {
+    case 16: return launch_rows<16>(a, p.blocks, st);
+    case 32: return launch_rows<32>(a, p.blocks, st);
+    case 64: return launch_rows<64>(a, p.blocks, st);
+    default: return launch_rows<128>(a, p.blocks, st);
+  }
 }
 
 }  // namespace tq

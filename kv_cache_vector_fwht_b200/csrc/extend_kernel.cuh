@@ -1,0 +1,882 @@
+// Attention of several query tokens over the packed cache on the tensor cores (sm_100a):
+// tq_extend_attention, and over listed blocks tq_decode_attention_blocks.
+//
+// Mathematics. For query row r (one token and one head of a KV head's group) and cached token i
+//   s_ri = n16_i ( <q'_r, c[idx_i]> + rho_i <Sq'_r, 2 sigma_i - 1> ) * const,   rho = r16 / n16,
+// so a token's packed key is ONE row of a matrix operand: the 128 level values of its codes and
+// (prod) 128 signs of size rho, and the token's norm is a factor of its whole row of scores. The
+// query side is [q' | Sq'] with q' = H (s . q), Sq' = S_rot q'. Both products of the attention run
+// on tcgen05 with the TOKENS along M:
+//   S^T [128 tokens x rows] = K' [128 x 128 or 256] . Q'^T      A = K' in tensor memory, B = Q' in shared memory
+//   O^T [128 channels x rows] += V^T [128 x 128 tokens] . P      A = V^T, B = P, both in shared memory
+// The rows (tokens x heads of the group) are N: a decode step with 8 heads costs an N = 16
+// product instead of a 128-row tile padded from 8, and the same kernel serves 1 to 128 rows.
+// A token is a lane: its norm, its mask position and its softmax weights live in one thread.
+//
+// One block of threads per SM works on one KV head, up to 128 query rows and a range of 128-token
+// tiles (two 64-token blocks each, listed or consecutive); its warps have roles:
+//   loader (1 warp)    packed rows of a tile to a shared ring by bulk copies, several tiles ahead;
+//   K (4 warps)        thread = token: codes to fp16 levels by byte permutes (packed.cuh), signs by
+//                      bit arithmetic, written to tensor memory (two buffers);
+//   V (4 warps)        thread = token: v = mn16 + code s16 in fp16 (code exact, one rounding), to
+//                      shared memory (two buffers); tokens past the end are zero rows;
+//   MMA (1 thread)     issues S^T of unit u, then O^T of unit u - 1;
+//   softmax (2 x 4)    two streams: the even and the odd tiles for up to 64 rows, the lower and the
+//                      upper 64 rows beyond. Each has its own score and output columns, reference
+//                      maxima and sums, so one's exponentials run under the other's products.
+// Softmax in base 2 relative to a reference per row that is raised only when a score exceeds
+// it by more than 8 (one vote a unit; then the stream's outputs in tensor memory and its sums
+// are scaled), so p <= 256 fits fp16. Statistics and sums in fp32. Rounded to fp16 (relative 2^-11
+// each): q', Sq' and rho, p, v; the levels are scaled by a common factor that makes them fp16
+// numbers to 2^-13 or better.
+//
+// Bounds: a long decode reads 164 bytes a token and KV head (4-bit keys and values) from HBM; the K
+// and V warps spend about 550 thread instructions a token on unpacking; a chunk of a prompt (128
+// rows) is bound by the tensor cores and the softmax's instructions.
+#pragma once
+
+#include <cmath>
+
+#include "packed.cuh"
+
+namespace tq {
+namespace ext {
+
+constexpr int kTile = 128;              // tokens of a tile
+constexpr int kThreads = 576;           // 18 warps
+constexpr int kWarpsAll = kThreads / 32;
+constexpr int kMaxStages = 6;
+constexpr int kMaxList = 64;            // sequences whose block counts are listed one by one
+constexpr float kTau = 8.f;             // a reference is raised when exceeded by this (base 2)
+constexpr float kNoRef = -1e30f;        // reference of a row that has seen nothing
+constexpr int kNowhere = 0x40000000;    // position of a token that does not exist
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kPartFloats = 132;        // partial record: m, l, 0, 0, o[128]
+
+struct ExtendArgs {
+  const uint8_t* k_idx;
+  const uint8_t* k_sgn;
+  const uint8_t* k_nrm;
+  const uint8_t* v_q;
+  const uint8_t* v_par;
+  const int32_t* len;
+  const int32_t* blocks;    // nullable: (sequence, KV head, n_select) listed blocks
+  const DevTables* tab;
+  const void* q;
+  void* out;
+  float* part;              // partial records, slot = block of threads
+  int* counters;
+  int* err;
+  int64_t qb, qh, qt, ob, oh, ot;
+  int q_dtype, out_dtype;
+  int batch, n_kv_heads, capacity, n_tokens, n_select, n_blocks, causal;
+  int row_tiles;            // tiles of N query rows of the KV head with most of them
+  int mode, bits0, bits1;   // code bits (grouped: outliers, then the others)
+  int idx_bytes, sgn_bytes, nrm_bytes, vq_bytes, vbits;
+  int stages, stage_bytes;
+  float key_scale0, key_scale1;   // level scale / sqrt(channels) of the groups
+  float sketch_ratio;       // rho = sketch_ratio * r16 / n16
+  float scale_log2;
+  int uniform_splits;       // batch > kMaxList: splits of every sequence
+  int first[kMaxList + 1];  // first block of threads of each sequence
+  int16_t splits[kMaxList];
+  HeadLists heads;
+};
+
+// Shared-memory plan for N query rows and K columns of the key operand.
+__host__ __device__ constexpr int stream_rows(int n) { return n < 64 ? n : 64; }
+__host__ __device__ constexpr int p_bytes(int n) { return stream_rows(n) / 8 * 2048; }
+constexpr int kVBytes = kTile * kD * 2;
+constexpr int kMiscBytes = 4096;
+__host__ __device__ constexpr int smem_fixed(int n, int k) { return n * k * 2 + 2 * kVBytes + 2 * p_bytes(n) + kMiscBytes; }
+
+struct Misc {
+  uint64_t raw_full[kMaxStages], raw_empty[kMaxStages];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], p_empty[2];
+  uint64_t rot, sq_in, sq_full, q_full;
+  uint32_t tmem;
+  int last;
+  int poison[4];            // per value group: lowest position of a non-finite cached value
+  unsigned qmax;            // largest finite squared norm of the rows (float bits)
+  int pos0[16][2];          // first position of a tile's two halves, by tile mod 16
+  alignas(16) int limit[128];   // per row: positions it attends to
+  alignas(16) float ref[2][64];
+  alignas(16) float fac[2][64];
+  alignas(16) float scal[4][kTile];   // per token of a tile: the factor of its scores, by tile mod 4
+};
+static_assert(sizeof(Misc) <= kMiscBytes, "misc fits");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+// Barrier of a stream's 128 threads that tells each whether any of them asked.
+__device__ __forceinline__ bool named_any(int id, bool ask) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(ask)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+// One warp's arrival after all of its lanes' writes.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+constexpr uint32_t kMnMajorAB = (1u << 15) | (1u << 16);   // instruction descriptor: A and B M/N-major
+
+// Operand position of rotated coordinate c (the inverse of level_channel) in a run of `bits`-bit codes.
+__device__ __forceinline__ int operand_position(int bits, int c) {
+  if (bits == 1) {
+    const int i = c & 31;
+    return (c & ~31) + (i < 16 ? 2 * i : 2 * (i - 16) + 1);
+  }
+  if (bits == 2) {
+    const int i = c & 15;
+    return (c & ~15) + (i & 1 ? 8 + (i >> 1) : i >> 1);
+  }
+  return c;
+}
+
+// Unpack 32 channels (WU index words) to 16 operand pairs; SCALED: times g.
+template <int BITS, bool SCALED>
+__device__ __forceinline__ void key_unit(const uint32_t* w, const Levels& lv, __half2 g, uint32_t tcol) {
+  uint32_t r[16];
+  constexpr int NP = level_pairs(BITS), WU = 16 / NP;
+#pragma unroll
+  for (int i = 0; i < WU; ++i) unpack_levels<BITS>(w[i], lv, *reinterpret_cast<uint32_t(*)[NP]>(r + NP * i));
+  if constexpr (SCALED) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = h2bits(__hmul2(bits_h2(r[i]), g));
+  }
+  tmem_st16(tcol, r);
+}
+template <int BITS>
+__device__ __forceinline__ void key_row(const uint8_t* row, const Levels& lv, uint32_t tcol) {
+  constexpr int WU = 16 / level_pairs(BITS);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    uint32_t w[WU];
+    if constexpr (WU == 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * u);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else if constexpr (WU == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(row + 8 * u);
+      w[0] = x.x; w[1] = x.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(row + 4 * u);
+    }
+    key_unit<BITS, false>(w, lv, __half2{}, tcol + 16 * u);
+  }
+}
+template <int BITS>
+__device__ __forceinline__ void key_group(const uint8_t* row, int units, const Levels& lv, __half2 g, uint32_t tcol) {
+  constexpr int WU = 16 / level_pairs(BITS);
+  for (int u = 0; u < units; ++u) {
+    uint32_t w[WU];
+#pragma unroll
+    for (int i = 0; i < WU; ++i) w[i] = reinterpret_cast<const uint32_t*>(row)[WU * u + i];
+    key_unit<BITS, true>(w, lv, g, tcol + 16 * u);
+  }
+}
+// Channel of operand position m of V^T: chunks of 8 positions, pairs (code i, code i + 4) of a
+// word of 4-bit codes, (code i, code i + 8) of 2-bit ones.
+__device__ __forceinline__ int value_channel(int vbits, int m) {
+  const int chunk = m >> 3, p = m & 7;
+  if (vbits == 4) return 8 * chunk + (p >> 1) + 4 * (p & 1);
+  return 16 * (chunk >> 1) + 4 * (chunk & 1) + (p >> 1) + 8 * (p & 1);
+}
+// Code pairs of a masked word field as exact fp16 numbers: 1024 + 2^k code, minus 1024, over 2^k.
+template <int K>
+__device__ __forceinline__ __half2 code_pair(uint32_t w, uint32_t mask) {
+  const __half2 t = bits_h2((w & mask) | 0x64006400u);
+  if constexpr (K == 0) return __hsub2(t, bits_h2(0x64006400u));
+  const __half2 inv = __float2half2_rn(1.f / (1 << K)), off = __float2half2_rn(-1024.f / (1 << K));
+  return __hfma2(t, inv, off);
+}
+
+// The rows of this thread's 32-token warp reduced: v[i] over the lanes, result i in the lanes
+// with lane / 2 == i (16 values in 16 exchanges).
+template <typename F>
+__device__ __forceinline__ float reduce16(float (&v)[16], int lane, F f) {
+#pragma unroll
+  for (int h = 8, m = 16; h >= 1; h >>= 1, m >>= 1) {
+    const bool up = lane & m;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float mine = up ? v[i + h] : v[i], theirs = up ? v[i] : v[i + h];
+      v[i] = f(mine, __shfl_xor_sync(kFull, theirs, m));
+    }
+  }
+  return f(v[0], __shfl_xor_sync(kFull, v[0], 1));
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ ExtendArgs a) {
+  constexpr int NS = stream_rows(N);          // rows of a stream
+  constexpr bool kByRows = N > 64;            // streams split the rows (else the tiles)
+  constexpr uint32_t kS0 = 256, kO0 = 384;    // tensor-memory columns: K' 0..255, S^T, O^T
+
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const bool prod = a.mode == TQ_MODE_PROD;
+  const int kcols = prod ? 2 * kD : kD;
+  uint8_t* sQ = smem;
+  uint8_t* sV = sQ + N * kcols * 2;
+  uint8_t* sP = sV + 2 * kVBytes;
+  Misc& ms = *reinterpret_cast<Misc*>(sP + 2 * p_bytes(N));
+  uint8_t* sRaw = reinterpret_cast<uint8_t*>(&ms) + kMiscBytes;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- which sequence, KV head, query rows and range of tiles
+  int b, local, n_splits;
+  if (a.batch <= kMaxList) {
+    b = 0;
+    while (static_cast<int>(blockIdx.x) >= a.first[b + 1]) ++b;
+    local = blockIdx.x - a.first[b];
+    n_splits = a.splits[b];
+  } else {
+    const int per = a.n_kv_heads * a.row_tiles * a.uniform_splits;
+    b = blockIdx.x / per;
+    local = blockIdx.x - b * per;
+    n_splits = a.uniform_splits;
+  }
+  const int item = local / n_splits, split = local - item * n_splits;
+  const int kv = item % a.n_kv_heads;
+  // the last rows see most of a causal context: they start first
+  const int rt = a.row_tiles - 1 - item / a.n_kv_heads;
+  const int head0 = a.heads.start[kv], group = a.heads.start[kv + 1] - head0;
+  const int row0 = rt * N;
+  const int rows = min(N, group * a.n_tokens - row0);
+  if (rows <= 0) return;
+  const int len = max(0, min(a.len[b], a.capacity));
+  const int shift = a.causal ? a.n_tokens - 1 : 0;
+  auto row_limit = [&](int r) {   // positions row r of this tile attends to
+    const int t = (row0 + r) / group;
+    return max(0, min(len, a.causal ? len - shift + t : len));
+  };
+  const int top = row_limit(rows - 1), low = row_limit(0);
+  const int64_t pair = static_cast<int64_t>(b) * a.n_kv_heads + kv;
+  const int32_t* list = a.blocks ? a.blocks + pair * a.n_select : nullptr;
+  const int all_tiles = list ? (len > 0 ? (a.n_select + 1) / 2 : 0) : (top + kTile - 1) / kTile;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * split / n_splits);
+  const int nt = static_cast<int>(static_cast<int64_t>(all_tiles) * (split + 1) / n_splits) - tile0;
+
+  if (warp == 16) {
+    tmem_alloc(&ms.tmem, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&ms.raw_full[i], 1);
+      mbar_init(&ms.raw_empty[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.k_full[i], 4);
+      mbar_init(&ms.k_empty[i], 1);
+      mbar_init(&ms.v_full[i], 4);
+      mbar_init(&ms.v_empty[i], 1);
+      mbar_init(&ms.s_full[i], 1);
+      mbar_init(&ms.p_full[i], 4);
+      mbar_init(&ms.p_empty[i], 1);
+    }
+    mbar_init(&ms.rot, 1);
+    mbar_init(&ms.sq_in, 8);
+    mbar_init(&ms.sq_full, 1);
+    mbar_init(&ms.q_full, 8);
+    ms.qmax = 0;
+    fence_mbar_init();
+  }
+  if (tid < 4) ms.poison[tid] = 0x7fffffff;
+  if (tid < N) ms.limit[tid] = tid < rows ? row_limit(tid) : 0;
+  if (tid < 128) ms.ref[tid >> 6][tid & 63] = kNoRef;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = ms.tmem;
+  const uint32_t tlane = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  const int units = kByRows ? 2 * nt : nt;
+  bool ok = true;
+
+  if (nt == 0) {
+    // nothing to attend to
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ K: thread = token
+    const Levels lv0 = load_levels(a.tab, 0), lv1 = load_levels(a.tab, 1);
+    const int tok = tid;
+    const int o_sgn = kTile * a.idx_bytes, o_nrm = o_sgn + kTile * a.sgn_bytes;
+    for (int j = 0; j < nt; ++j) {
+      const int st = j % a.stages, kb = j & 1;
+      const uint8_t* raw = sRaw + st * a.stage_bytes;
+      if (ok) ok = mbar_wait_ns(&ms.raw_full[st], (j / a.stages) & 1, kWaitNs);
+      if (ok && j >= 2) ok = mbar_wait_ns(&ms.k_empty[kb], ((j >> 1) - 1) & 1, kWaitNs);
+      tc_fence_after();
+      const uint32_t tk = tlane + 128 * kb;
+      const uint8_t* row = raw + tok * a.idx_bytes;
+      float scal;
+      if (a.mode == TQ_MODE_GROUPED) {
+        const uint32_t nn = *reinterpret_cast<const uint32_t*>(raw + o_nrm + 4 * tok);
+        const float s0 = half_lo(nn) * a.key_scale0, s1 = half_hi(nn) * a.key_scale1;
+        scal = fmaxf(s0, s1);
+        const float inv = scal > 0.f ? 1.f / scal : 0.f;
+        const __half2 g0 = __float2half2_rn(s0 * inv), g1 = __float2half2_rn(s1 * inv);
+        const uint8_t* rest = row + 4 * storage_width_c(a.bits0);
+        if (a.bits1 == 1) {
+          key_group<2>(row, 1, lv0, g0, tk);
+          key_group<1>(rest, 3, lv1, g1, tk + 16);
+        } else if (a.bits1 == 2) {
+          key_group<3>(row, 1, lv0, g0, tk);
+          key_group<2>(rest, 3, lv1, g1, tk + 16);
+        } else {
+          key_group<4>(row, 1, lv0, g0, tk);
+          key_group<3>(rest, 3, lv1, g1, tk + 16);
+        }
+      } else {
+        switch (a.bits0) {
+          case 1: key_row<1>(row, lv0, tk); break;
+          case 2: key_row<2>(row, lv0, tk); break;
+          case 3: key_row<3>(row, lv0, tk); break;
+          default: key_row<4>(row, lv0, tk); break;
+        }
+        if (prod) {
+          const uint32_t nn = *reinterpret_cast<const uint32_t*>(raw + o_nrm + 4 * tok);
+          const float n16 = half_lo(nn);
+          const uint32_t rho = h2bits(__float2half2_rn(n16 > 0.f ? half_hi(nn) / n16 * a.sketch_ratio : 0.f));
+          scal = n16 * a.key_scale0;
+          const uint4 sg = *reinterpret_cast<const uint4*>(raw + o_sgn + 16 * tok);
+          const uint32_t inv[4] = {~sg.x, ~sg.y, ~sg.z, ~sg.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t r[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = sign_level(inv[u], i, rho);
+            tmem_st16(tk + 64 + 16 * u, r);
+          }
+        } else {
+          scal = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(raw + o_nrm + 2 * tok))) * a.key_scale0;
+        }
+      }
+      ms.scal[j & 3][tok] = scal;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ms.raw_empty[st]);
+        mbar_arrive(&ms.k_full[kb]);
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ V: thread = token
+    const int tok = tid - 128;
+    const int o_vq = kTile * (a.idx_bytes + a.sgn_bytes + a.nrm_bytes), o_par = o_vq + kTile * a.vq_bytes;
+    for (int j = 0; j < nt; ++j) {
+      const int st = j % a.stages, vb = j & 1;
+      const uint8_t* raw = sRaw + st * a.stage_bytes;
+      if (ok) ok = mbar_wait_ns(&ms.raw_full[st], (j / a.stages) & 1, kWaitNs);
+      if (ok && j >= 2) ok = mbar_wait_ns(&ms.v_empty[vb], ((j >> 1) - 1) & 1, kWaitNs);
+      // the second buffer holds the sketch matrix until S q has been formed
+      if (ok && j == 1 && prod) ok = mbar_wait_ns(&ms.sq_full, 0, kWaitNs);
+      const int pos = ms.pos0[j & 15][tok >> 6] + (tok & 63);
+      const bool there = pos < len;
+      const uint4 par = *reinterpret_cast<const uint4*>(raw + o_par + 16 * tok);
+      const uint32_t pw[4] = {par.x, par.y, par.z, par.w};
+      uint8_t* dst = sV + vb * kVBytes + tok * 16;
+      const uint8_t* src = raw + o_vq + tok * a.vq_bytes;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t p = there ? pw[g] : 0u;
+        if ((p & 0x7c00u) == 0x7c00u || (p & 0x7c000000u) == 0x7c000000u) {
+          // inf or NaN: 0 * inf would reach rows that may not see this token, so the product gets zeros and
+          // the rows that do see it are set to NaN at the end
+          atomicMin(&ms.poison[g], pos);
+          p = 0;
+        }
+        const __half2 mn = __half2half2(__low2half(bits_h2(p))), sc = __half2half2(__high2half(bits_h2(p)));
+        if (a.vbits == 4) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(src + 16 * g);
+          const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = ws[i], v = w >> 8;
+            uint4 o;
+            o.x = h2bits(__hfma2(code_pair<0>(w, 0x000f000fu), sc, mn));
+            o.y = h2bits(__hfma2(code_pair<4>(w, 0x00f000f0u), sc, mn));
+            o.z = h2bits(__hfma2(code_pair<0>(v, 0x000f000fu), sc, mn));
+            o.w = h2bits(__hfma2(code_pair<4>(v, 0x00f000f0u), sc, mn));
+            *reinterpret_cast<uint4*>(dst + (4 * g + i) * 2048) = o;
+          }
+        } else {
+          const uint2 w2 = *reinterpret_cast<const uint2*>(src + 8 * g);
+          const uint32_t ws[2] = {w2.x, w2.y};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = ws[i], v = w >> 8;
+            uint4 o;
+            o.x = h2bits(__hfma2(code_pair<0>(w, 0x00030003u), sc, mn));
+            o.y = h2bits(__hfma2(code_pair<2>(w, 0x000c000cu), sc, mn));
+            o.z = h2bits(__hfma2(code_pair<4>(w, 0x00300030u), sc, mn));
+            o.w = h2bits(__hfma2(code_pair<6>(w, 0x00c000c0u), sc, mn));
+            *reinterpret_cast<uint4*>(dst + (4 * g + 2 * i) * 2048) = o;
+            o.x = h2bits(__hfma2(code_pair<0>(v, 0x00030003u), sc, mn));
+            o.y = h2bits(__hfma2(code_pair<2>(v, 0x000c000cu), sc, mn));
+            o.z = h2bits(__hfma2(code_pair<4>(v, 0x00300030u), sc, mn));
+            o.w = h2bits(__hfma2(code_pair<6>(v, 0x00c000c0u), sc, mn));
+            *reinterpret_cast<uint4*>(dst + (4 * g + 2 * i + 1) * 2048) = o;
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ms.raw_empty[st]);
+        mbar_arrive(&ms.v_full[vb]);
+      }
+    }
+  } else if (warp == 17) {
+    // ------------------------------------------------------------------ loader
+    if (prod && lane == 0) {
+      mbar_expect_tx(&ms.rot, kD * kD * 2);
+      bulk_g2s(sV + kVBytes, a.tab->s_umma, kD * kD * 2, &ms.rot);
+    }
+    const int o_sgn = kTile * a.idx_bytes, o_nrm = o_sgn + kTile * a.sgn_bytes, o_vq = o_nrm + kTile * a.nrm_bytes,
+              o_par = o_vq + kTile * a.vq_bytes;
+    // lane = plane + 5 * half
+    const int plane = lane % 5, half = lane / 5;
+    const uint8_t* base = plane == 0 ? a.k_idx : plane == 1 ? a.k_sgn : plane == 2 ? a.k_nrm : plane == 3 ? a.v_q : a.v_par;
+    const int rb = plane == 0 ? a.idx_bytes : plane == 1 ? a.sgn_bytes : plane == 2 ? a.nrm_bytes : plane == 3 ? a.vq_bytes : 16;
+    const int off = plane == 0 ? 0 : plane == 1 ? o_sgn : plane == 2 ? o_nrm : plane == 3 ? o_vq : o_par;
+    const int row_bytes = a.idx_bytes + a.sgn_bytes + a.nrm_bytes + a.vq_bytes + 16;
+    int done = 0;
+    for (int j = 0; j < nt && ok; ++j, ++done) {
+      const int st = j % a.stages;
+      if (j >= a.stages) ok = mbar_wait_ns(&ms.raw_empty[st], (j / a.stages - 1) & 1, kWaitNs);
+      if (!ok) break;
+      int p[2], n[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = 2 * (tile0 + j) + h;
+        int blk = i;
+        if (list) blk = i < a.n_select ? __ldg(list + i) : -1;
+        const bool in = blk >= 0 && blk < a.n_blocks && blk * TQ_BLOCK < len;
+        p[h] = in ? blk * TQ_BLOCK : kNowhere;
+        n[h] = in ? min(TQ_BLOCK, (len - blk * TQ_BLOCK + 15) & ~15) : 0;   // within the capacity, a multiple of 16
+      }
+      if (lane == 0) {
+        ms.pos0[j & 15][0] = p[0];
+        ms.pos0[j & 15][1] = p[1];
+        mbar_expect_tx(&ms.raw_full[st], (n[0] + n[1]) * row_bytes);
+      }
+      __syncwarp();
+      const int mine = half == 0 ? n[0] : n[1], from = half == 0 ? p[0] : p[1];
+      if (lane < 10 && mine > 0 && rb > 0)
+        bulk_g2s(sRaw + st * a.stage_bytes + off + half * TQ_BLOCK * rb,
+                 base + (pair * a.capacity + from) * rb, mine * rb, &ms.raw_full[st]);
+    }
+    // if another role gave up, wait here for the copies that nothing else will wait for
+    for (int j = max(0, done - a.stages); j < done; ++j)
+      mbar_wait_ns(&ms.raw_full[j % a.stages], (j / a.stages) & 1, kWaitNs);
+  } else if (warp == 16) {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0) {
+      const uint32_t qsbo = 16u * kcols;   // bytes of 8 query rows
+      if (prod) {
+        // S q: D [128 x N] = S_rot [128 x 128] . q'^T, the rows' copy in the sketch's column order
+        ok = mbar_wait_ns(&ms.rot, 0, kWaitNs);
+        if (ok) ok = mbar_wait_ns(&ms.sq_in, 0, kWaitNs);
+        if (ok) {
+          tc_fence_after();
+          for (int s = 0; s < 8; ++s)
+            umma_f16(tbase + kS0, umma_desc(smem_u32(sV + kVBytes) + 256 * s, 128, 2048),
+                     umma_desc(smem_u32(sP) + 256 * s, 128, 2048), umma_idesc_f16(128, N), s > 0);
+          umma_commit(&ms.sq_full);
+        }
+      }
+      if (ok) ok = mbar_wait_ns(&ms.q_full, 0, kWaitNs);
+      for (int u = 0; u <= units && ok; ++u) {
+        if (u < units) {
+          const int s = u & 1, j = kByRows ? u >> 1 : u, kb = j & 1;
+          if (!kByRows || s == 0) ok = mbar_wait_ns(&ms.k_full[kb], (j >> 1) & 1, kWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t bq = smem_u32(sQ) + (kByRows ? s * (NS / 8) * qsbo : 0);
+          const int steps = kcols / 16;
+          for (int k = 0; k < steps; ++k)
+            umma_f16_ts(tbase + kS0 + 64 * s, tbase + 128 * kb + 8 * k, umma_desc(bq + 256 * k, 128, qsbo),
+                        umma_idesc_f16(128, NS), k > 0);
+          umma_commit(&ms.s_full[s]);
+          if (!kByRows || s == 1) umma_commit(&ms.k_empty[kb]);
+        }
+        if (u > 0) {
+          const int w = u - 1, s = w & 1, i = w >> 1, j = kByRows ? w >> 1 : w, vb = j & 1;
+          if (!kByRows || s == 0) ok = mbar_wait_ns(&ms.v_full[vb], (j >> 1) & 1, kWaitNs);
+          if (ok) ok = mbar_wait_ns(&ms.p_full[s], i & 1, kWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          for (int k = 0; k < 8; ++k)
+            umma_f16(tbase + kO0 + 64 * s, umma_desc(smem_u32(sV) + vb * kVBytes + 256 * k, 128, 2048),
+                     umma_desc(smem_u32(sP) + s * p_bytes(N) + 256 * k, 128, 2048),
+                     umma_idesc_f16(128, NS) | kMnMajorAB, i > 0 || k > 0);
+          umma_commit(&ms.p_empty[s]);
+          if (!kByRows || s == 1) umma_commit(&ms.v_empty[vb]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax streams
+    const int s = (warp - 8) >> 2, tok = (warp & 3) * 32 + lane;
+    uint8_t* myP = sP + s * p_bytes(N);
+    float qscale;
+    {  // ---- the query operand: rotated rows, and S q for prod; 8 warps
+      const int w8 = warp - 8;
+      auto load_row = [&](int r, float (&v)[4]) {
+        const int t = (row0 + r) / group, h = a.heads.head[head0 + (row0 + r) - t * group];
+        const int64_t at = b * a.qb + h * a.qh + t * a.qt;
+        if (a.mode == TQ_MODE_GROUPED) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = load_element(a.q, a.q_dtype, at + a.tab->chan[4 * lane + i]);
+        } else if (a.q_dtype == TQ_F32) {
+          load4<true>(static_cast<const float*>(a.q) + at, 4 * lane, v);
+        } else if (a.q_dtype == TQ_BF16) {
+          load4<false>(static_cast<const uint16_t*>(a.q) + at, 4 * lane, v);
+        } else {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at) + lane);
+          v[0] = half_lo(x.x); v[1] = half_hi(x.x); v[2] = half_lo(x.y); v[3] = half_hi(x.y);
+        }
+      };
+      for (int r = w8; r < rows; r += 8) {
+        float v[4];
+        load_row(r, v);
+        const float n2 = warp_sum(v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3]);
+        if (lane == 0 && n2 < INFINITY) atomicMax(&ms.qmax, __float_as_uint(n2));
+      }
+      named_sync(3, 256);
+      // a power of two that brings the longest row to a norm of 8 .. 16 (the other rows are shorter)
+      const float n2 = __uint_as_float(ms.qmax);
+      const int e = n2 > 0.f ? (ilogbf(n2) >> 1) - 3 : 0;
+      const float down = exp2f(static_cast<float>(-max(-120, min(120, e))));
+      qscale = a.scale_log2 / down;
+      const uint32_t sbits = a.tab->sign_bits[lane >> 3] >> (4 * (lane & 7));
+      const float unit = down * (a.mode == TQ_MODE_GROUPED ? 0.17677669529663688f : 0.08838834764831845f);
+      for (int r = w8; r < N; r += 8) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r < rows) load_row(r, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = flip_sign(v[i] * unit, sbits, i);
+        fwht_reg<4>(v);
+#pragma unroll
+        for (int m = 1; m <= 16; m <<= 1) {
+          if (m == 8 && a.mode == TQ_MODE_GROUPED) break;   // 32-point blocks
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float o = __shfl_xor_sync(kFull, v[i], m);
+            v[i] = lane & m ? o - v[i] : v[i] + o;
+          }
+        }
+        uint8_t* qrow = sQ + (r >> 3) * 16 * kcols + (r & 7) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = 4 * lane + i;
+          const int k = a.mode != TQ_MODE_GROUPED ? operand_position(a.bits0, c)
+                        : c < 32                  ? operand_position(a.bits0, c)
+                                                  : 32 + operand_position(a.bits1, c - 32);
+          const __half h = __float2half_rn(v[i]);
+          *reinterpret_cast<__half*>(qrow + (k >> 3) * 128 + (k & 7) * 2) = h;
+          if (prod) {
+            const int k2 = c < 64 ? 2 * c : 2 * (c - 64) + 1;
+            *reinterpret_cast<__half*>(sP + (r >> 3) * 2048 + (r & 7) * 16 + (k2 >> 3) * 128 + (k2 & 7) * 2) = h;
+          }
+        }
+      }
+      fence_async_smem();
+      if (prod) {
+        warp_arrive(&ms.sq_in, lane);
+        ok = mbar_wait_ns(&ms.sq_full, 0, kWaitNs);
+        tc_fence_after();
+        // lane = sketch row j; a stream's warps take half of the query rows
+        const int k = kD + operand_position(1, tok);
+        for (int c = 0; c < N / 2; c += 8) {
+          uint32_t x[16];
+          const int n0 = s * (N / 2) + c;
+          if (c % 16 == 0 || N / 2 < 16) {
+            tmem_ld16_sync(tlane + kS0 + (N / 2 < 16 ? 0 : n0), x);
+          }
+          const int skip = N / 2 < 16 ? n0 : 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int n = N / 2 < 16 ? i : n0 + i;
+            if (N / 2 < 16 && (i < skip || i >= skip + 8)) continue;
+            *reinterpret_cast<__half*>(sQ + (n >> 3) * 16 * kcols + (n & 7) * 16 + (k >> 3) * 128 + (k & 7) * 2) =
+                __float2half_rn(__uint_as_float(x[i]) * 0.125f);
+          }
+          if (N / 2 >= 16) c += 8;
+        }
+        tc_fence_before();
+        fence_async_smem();
+      }
+      warp_arrive(&ms.q_full, lane);
+    }
+
+    float sum[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) sum[i] = 0.f;
+    const int r_first = kByRows ? s * NS : 0;          // this stream's rows of the tile
+    const int* limit = ms.limit + r_first;
+    float* ref = ms.ref[s];
+    const int mine = kByRows ? nt : (nt - s + 1) / 2;  // this stream's units
+    const uint32_t tS = tlane + kS0 + 64 * s, tO = tlane + kO0 + 64 * s;
+    const int lowest = kByRows ? row_limit(min(r_first, rows - 1)) : low;
+    for (int i = 0; i < mine; ++i) {
+      const int j = kByRows ? i : 2 * i + s;
+      if (ok) ok = mbar_wait_ns(&ms.s_full[s], i & 1, kWaitNs);
+      tc_fence_after();
+      const float sc = ms.scal[j & 3][tok] * qscale;
+      const int pos = ms.pos0[j & 15][tok >> 6] + (tok & 63);
+      const bool masked = __any_sync(kFull, pos >= lowest);
+      bool waited = i == 0;
+      // logits (base 2) of 16 rows, masked ones -inf, relative to base
+      auto logits = [&](int c, bool rel, float (&x)[16]) {
+        uint32_t y[16];
+        tmem_ld16_sync(tS + c, y);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 m4 = rel ? *reinterpret_cast<const float4*>(ref + c + 4 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[4 * q] = fmaf(__uint_as_float(y[4 * q]), sc, -m4.x);
+          x[4 * q + 1] = fmaf(__uint_as_float(y[4 * q + 1]), sc, -m4.y);
+          x[4 * q + 2] = fmaf(__uint_as_float(y[4 * q + 2]), sc, -m4.z);
+          x[4 * q + 3] = fmaf(__uint_as_float(y[4 * q + 3]), sc, -m4.w);
+        }
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int4 l4 = *reinterpret_cast<const int4*>(limit + c + 4 * q);
+            x[4 * q] = pos < l4.x ? x[4 * q] : -INFINITY;
+            x[4 * q + 1] = pos < l4.y ? x[4 * q + 1] : -INFINITY;
+            x[4 * q + 2] = pos < l4.z ? x[4 * q + 2] : -INFINITY;
+            x[4 * q + 3] = pos < l4.w ? x[4 * q + 3] : -INFINITY;
+          }
+        }
+      };
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < NS; c += 16) {
+        float x[16];
+        logits(c, true, x);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) mx = fmaxf(mx, x[q]);
+      }
+      if (named_any(1 + s, mx > kTau)) {
+        // raise the references to the tile's maxima
+        if (!waited && ok) ok = mbar_wait_ns(&ms.p_empty[s], (i - 1) & 1, kWaitNs);
+        waited = true;
+        tc_fence_after();
+        float* wmax = reinterpret_cast<float*>(myP);   // free: the last product has read it
+#pragma unroll
+        for (int c = 0; c < NS; c += 16) {
+          float x[16];
+          logits(c, false, x);
+          const float m = reduce16(x, lane, [](float p, float q) { return fmaxf(p, q); });
+          if ((lane & 1) == 0) wmax[(warp & 3) * NS + c + (lane >> 1)] = m;
+        }
+        named_sync(1 + s, 128);
+        if (tok < NS) {
+          const float old = ref[tok];
+          const float m = fmaxf(fmaxf(old, fmaxf(wmax[tok], wmax[NS + tok])), fmaxf(wmax[2 * NS + tok], wmax[3 * NS + tok]));
+          ms.fac[s][tok] = old == m ? 1.f : ex2(old - m);
+          ref[tok] = m;
+        }
+        named_sync(1 + s, 128);
+        const float* fac = ms.fac[s];
+#pragma unroll
+        for (int c = 0; c < NS; ++c) sum[c] *= fac[c];
+        if (i > 0) {
+#pragma unroll
+          for (int c = 0; c < NS; c += 16) {
+            uint32_t o[16];
+            tmem_ld16_sync(tO + c, o);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * fac[c + q]);
+            tmem_st16(tO + c, o);
+          }
+          tmem_st_wait();
+        }
+      }
+      if (!waited && ok) ok = mbar_wait_ns(&ms.p_empty[s], (i - 1) & 1, kWaitNs);
+#pragma unroll
+      for (int c = 0; c < NS; c += 16) {
+        float x[16];
+        logits(c, true, x);
+        uint32_t p[8];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          x[q] = ex2(x[q]);
+          sum[c + q] += x[q];
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) p[q] = h2bits(__floats2half2_rn(x[2 * q], x[2 * q + 1]));
+        *reinterpret_cast<uint4*>(myP + (c >> 3) * 2048 + tok * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+        *reinterpret_cast<uint4*>(myP + ((c >> 3) + 1) * 2048 + tok * 16) = make_uint4(p[4], p[5], p[6], p[7]);
+      }
+      fence_async_smem();
+      tc_fence_before();
+      warp_arrive(&ms.p_full[s], lane);
+    }
+
+    // ---- join the stream's 128 tokens' sums, then the streams
+    if (mine > 0 && ok) ok = mbar_wait_ns(&ms.p_empty[s], (mine - 1) & 1, kWaitNs);
+    tc_fence_after();
+    float* wsum = reinterpret_cast<float*>(myP);
+#pragma unroll
+    for (int c = 0; c < NS; c += 16) {
+      float x[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) x[q] = sum[c + q];
+      const float t = reduce16(x, lane, [](float p, float q) { return p + q; });
+      if ((lane & 1) == 0) wsum[(warp & 3) * NS + c + (lane >> 1)] = t;
+    }
+    named_sync(3, 256);
+    // factors of the two streams and the joint maximum and sum (by rows: of this stream alone)
+    float* join = reinterpret_cast<float*>(&ms.scal[0][0]);   // [stream][64] factor, then m and l: free now
+    if (tok < NS) {
+      const float* w0 = reinterpret_cast<float*>(sP);
+      const float* w1 = reinterpret_cast<float*>(sP + p_bytes(N));
+      const float l0 = (w0[tok] + w0[NS + tok]) + (w0[2 * NS + tok] + w0[3 * NS + tok]);
+      const float l1 = (w1[tok] + w1[NS + tok]) + (w1[2 * NS + tok] + w1[3 * NS + tok]);
+      if (kByRows) {
+        join[128 + s * 64 + tok] = ref[tok];
+        join[256 + s * 64 + tok] = s ? l1 : l0;
+        join[s * 64 + tok] = 1.f;
+      } else if (s == 0) {
+        const float m0 = ms.ref[0][tok], m1 = ms.ref[1][tok], m = fmaxf(m0, m1);
+        const float f0 = m0 == m ? 1.f : ex2(m0 - m), f1 = m1 == m ? 1.f : ex2(m1 - m);
+        join[tok] = f0;
+        join[64 + tok] = f1;
+        join[128 + tok] = m;
+        join[256 + tok] = l0 * f0 + l1 * f1;
+      }
+    }
+    named_sync(3, 256);
+    float* xbuf = reinterpret_cast<float*>(sV);   // [row][operand position], the other stream's outputs
+    const int both = kByRows ? 0 : (nt > 1);
+    if (both && s == 1) {
+#pragma unroll
+      for (int c = 0; c < NS; c += 16) {
+        uint32_t o[16];
+        tmem_ld16_sync(tO + c, o);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) xbuf[(c + q) * kD + tok] = __uint_as_float(o[q]) * join[64 + c + q];
+      }
+    }
+    if (both) named_sync(3, 256);
+    if (kByRows || s == 0) {
+      const int ch = value_channel(a.vbits, tok);
+      const int poison = ms.poison[ch >> 5];
+#pragma unroll
+      for (int c = 0; c < NS; c += 16) {
+        uint32_t o[16];
+        tmem_ld16_sync(tO + c, o);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const int r = r_first + c + q;
+          if (r >= rows) continue;
+          float v = __uint_as_float(o[q]) * join[r_first + c + q];
+          if (both) v += xbuf[(c + q) * kD + tok];
+          const float l = join[256 + r_first + c + q];
+          if (poison < ms.limit[r]) v = __uint_as_float(0x7fffffffu);
+          if (n_splits == 1) {
+            const int t = (row0 + r) / group, h = a.heads.head[head0 + (row0 + r) - t * group];
+            store_element(a.out, a.out_dtype, b * a.ob + h * a.oh + t * a.ot + ch, l == 0.f ? 0.f : v / l);
+          } else {
+            float* rec = a.part + (static_cast<int64_t>(blockIdx.x) * N + r) * kPartFloats;
+            rec[4 + ch] = v;
+            if (tok == 0) {
+              rec[0] = join[128 + r];
+              rec[1] = l;
+            }
+          }
+        }
+      }
+    }
+  }
+
+  if (!ok) atomicOr(a.err, 1);
+  __syncwarp();
+  tc_fence_before();
+  if (nt == 0 && tid >= 256 && tid < 384) {   // no tokens: zeros, or an empty record
+    const int ch = tid - 256;
+    for (int r = 0; r < rows; ++r) {
+      if (n_splits == 1) {
+        const int t = (row0 + r) / group, h = a.heads.head[head0 + (row0 + r) - t * group];
+        store_element(a.out, a.out_dtype, b * a.ob + h * a.oh + t * a.ot + ch, 0.f);
+      } else if (ch < 2) {
+        a.part[(static_cast<int64_t>(blockIdx.x) * N + r) * kPartFloats + ch] = ch ? 0.f : kNoRef;
+      }
+    }
+  }
+  if (n_splits > 1) __threadfence();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+  if (n_splits == 1) return;
+
+  // ---- the last block of threads of this item joins the splits, in their order
+  const int first = blockIdx.x - split;
+  if (tid == 0) {
+    int* counter = a.counters + first;
+    ms.last = atomicAdd(counter, 1) == n_splits - 1;
+    if (ms.last) *counter = 0;
+  }
+  __syncthreads();
+  if (!ms.last) return;
+  __threadfence();
+  for (int r = warp; r < rows; r += kWarpsAll) {
+    const float* rec = a.part + (static_cast<int64_t>(first) * N + r) * kPartFloats;
+    constexpr int64_t step = static_cast<int64_t>(N) * kPartFloats;
+    float M = kNoRef;
+    for (int i = lane; i < n_splits; i += 32) M = fmaxf(M, __ldcg(rec + i * step));
+    M = warp_max(M);
+    float L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n_splits; i0 += 4) {
+      float m[4], l[4];
+      float4 o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i0 + i < n_splits) {
+          const float* p = rec + (i0 + i) * step;
+          m[i] = __ldcg(p);
+          l[i] = __ldcg(p + 1);
+          o[i] = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i0 + i >= n_splits || m[i] == kNoRef) continue;   // an empty record has no outputs
+        const float f = m[i] == M ? 1.f : ex2(m[i] - M);
+        L = fmaf(f, l[i], L);
+        O.x = fmaf(f, o[i].x, O.x); O.y = fmaf(f, o[i].y, O.y);
+        O.z = fmaf(f, o[i].z, O.z); O.w = fmaf(f, o[i].w, O.w);
+      }
+    }
+    const int t = (row0 + r) / group, h = a.heads.head[head0 + (row0 + r) - t * group];
+    const int64_t at = b * a.ob + h * a.oh + t * a.ot + 4 * lane;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    store_element(a.out, a.out_dtype, at, O.x * inv);
+    store_element(a.out, a.out_dtype, at + 1, O.y * inv);
+    store_element(a.out, a.out_dtype, at + 2, O.z * inv);
+    store_element(a.out, a.out_dtype, at + 3, O.w * inv);
+  }
+}
+
+}  // namespace ext
+}  // namespace tq

@@ -19,27 +19,14 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return d;
 }
 
-// Levels of a codebook of `bits`-bit codes: bytes of the fp16 levels (4 bits: of the upper,
-// positive half; 1 bit: lo[0] is the positive level twice).
+// Byte pools of a codebook (DevTables::lv_lo, lv_hi): the levels over DevTables::lv_scale in fp16
+// (4-bit codes: the positive half; 1-bit: lo[0] is the positive level twice).
 struct Levels {
   uint32_t lo[2], hi[2];
 };
 
-// cent: the fp32 levels, ascending and mirrored; the table holds cent * scale rounded to fp16.
-__device__ __forceinline__ Levels make_levels(const float* cent, int bits, float scale) {
-  Levels t{{0, 0}, {0, 0}};
-  if (bits == 1) {
-    const uint32_t h = half_bits(__float2half_rn(cent[1] * scale));
-    t.lo[0] = h | (h << 16);
-    return t;
-  }
-  const int n = bits == 2 ? 4 : 8, first = bits == 4 ? 8 : 0;
-  for (int k = 0; k < n; ++k) {
-    const uint32_t h = half_bits(__float2half_rn(cent[first + k] * scale));
-    t.lo[k >> 2] |= (h & 0xffu) << (8 * (k & 3));
-    t.hi[k >> 2] |= (h >> 8) << (8 * (k & 3));
-  }
-  return t;
+__device__ __forceinline__ Levels load_levels(const DevTables* t, int group) {
+  return Levels{{t->lv_lo[group][0], t->lv_lo[group][1]}, {t->lv_hi[group][0], t->lv_hi[group][1]}};
 }
 
 // fp16 pairs a 32-bit index word of `bits`-bit codes gives

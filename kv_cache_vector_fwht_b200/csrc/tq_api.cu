@@ -1,4 +1,6 @@
 // C ABI of libtq (include/tq.h): argument checks on the host, then kernel launches.
+#include <algorithm>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <new>
@@ -173,6 +175,36 @@ void gather_schedule(const int32_t (&chan)[tq::kD], uint8_t (&sched)[32][4]) {
     }
   }
 }
+// The byte pools of DevTables::lv_lo / lv_hi for the codebook `cent` (2^bits mirrored levels). Of
+// 4096 factors in [1, 2) the one is taken whose products with the levels are nearest to fp16
+// numbers, so that rounding the levels costs next to nothing (a level alone may be 2^-12 off).
+float level_bytes(const double* cent, int bits, uint32_t (&lo)[2], uint32_t (&hi)[2]) {
+  const int n = 1 << bits, half = n / 2;
+  double best = 1.0, best_err = 1e300;
+  for (int g = 0; g < 4096; ++g) {
+    const double f = 1.0 + g / 4096.0;
+    double err = 0.0;
+    for (int k = half; k < n; ++k) {
+      const double x = cent[k] * f;
+      const double ulp = std::ldexp(1.0, std::ilogb(x) - 10);   // fp16 spacing at x
+      err = std::max(err, std::fabs(std::nearbyint(x / ulp) * ulp - x) / x);
+    }
+    if (err < best_err) { best_err = err; best = f; }
+  }
+  lo[0] = lo[1] = hi[0] = hi[1] = 0;
+  if (bits == 1) {
+    const uint32_t h = float_to_half_bits_rn(cent[1] * best);
+    lo[0] = h | (h << 16);
+  } else {
+    const int first = bits == 4 ? half : 0, count = bits == 4 ? half : n;
+    for (int k = 0; k < count; ++k) {
+      const uint32_t h = float_to_half_bits_rn(cent[first + k] * best);
+      lo[k >> 2] |= (h & 0xffu) << (8 * (k & 3));
+      hi[k >> 2] |= (h >> 8) << (8 * (k & 3));
+    }
+  }
+  return static_cast<float>(1.0 / best);
+}
 }  // namespace
 
 static tq_status build_quantizer(int d, int bits, int mode, uint64_t seed,
@@ -232,6 +264,10 @@ static tq_status build_quantizer(int d, int bits, int mode, uint64_t seed,
       }
   }
   if (mode == TQ_MODE_GROUPED) gather_schedule(q->host.chan, h->gsched);
+  const int bits0 = mode == TQ_MODE_PROD ? bits - 1 : mode == TQ_MODE_GROUPED ? bits + 1 : bits;
+  h->lv_scale[0] = q->lv_scale[0] = level_bytes(q->host.cent[0], bits0, h->lv_lo[0], h->lv_hi[0]);
+  if (mode == TQ_MODE_GROUPED)
+    h->lv_scale[1] = q->lv_scale[1] = level_bytes(q->host.cent[1], bits, h->lv_lo[1], h->lv_hi[1]);
   for (int qq = 0; qq < kD / 2; ++qq)
     h->pair_mask[qq] = (q->host.signs[2 * qq] < 0 ? 1u << 15 : 0u) |
                        (q->host.signs[2 * qq + 1] < 0 ? 1u << 31 : 0u);

@@ -39,6 +39,11 @@ struct DevTables {
   // channels 4l .. 4l + 3; in store round k it writes channel 4l + gsched[l][k], chosen so that
   // the 32 lanes of a round write 32 different shared-memory banks.
   uint8_t gsched[32][4];
+  // fp16 levels of the codebooks as byte pools for permute lookups (packed.cuh): the level set
+  // (4-bit codes: its positive half; 1-bit: the positive level twice in lv_lo[0]) divided by
+  // lv_scale, a factor chosen so that every level is an fp16 number to 2^-13 or better.
+  uint32_t lv_lo[2][2], lv_hi[2][2];
+  float lv_scale[2];
 };
 
 struct HostTables {
@@ -61,6 +66,7 @@ struct tq_quantizer {
   uint64_t seed;
   tq_key_layout_t layout;
   tq::HostTables host;
+  float lv_scale[2];    // host copy of DevTables::lv_scale
   tq::DevTables* dev;   // device copy
   int device;           // CUDA device the copy lives on
 };
