@@ -486,17 +486,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       mbar_wait_ns(&ms.raw_full[j % a.stages], (j / a.stages) & 1, kWaitNs);
   } else if (warp == 16) {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t qsbo = 16u * kcols;   // bytes of 8 query rows
+      const uint64_t q_desc = umma_desc(smem_u32(sQ), 128, qsbo);
+      const uint64_t v_desc = umma_desc(smem_u32(sV), 128, 2048), p_desc = umma_desc(smem_u32(sP), 128, 2048);
       if (prod) {
         // S q: D [128 x N] = S_rot [128 x 128] . q'^T, the rows' copy in the sketch's column order
         ok = mbar_wait_ns(&ms.rot, 0, kWaitNs);
         if (ok) ok = mbar_wait_ns(&ms.sq_in, 0, kWaitNs);
         if (ok) {
           tc_fence_after();
-          for (int s = 0; s < 8; ++s)
-            umma_f16(tbase + kS0, umma_desc(smem_u32(sV + kVBytes) + 256 * s, 128, 2048),
-                     umma_desc(smem_u32(sP) + 256 * s, 128, 2048), umma_idesc_f16(128, N), s > 0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)   // 16 columns a step: two core matrices of 128 bytes
+            umma_f16(tbase + kS0, v_desc + (kVBytes >> 4) + 16 * k, p_desc + 16 * k, umma_idesc_f16(128, N), k > 0);
           umma_commit(&ms.sq_full);
         }
       }
@@ -507,11 +509,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           if (!kByRows || s == 0) ok = mbar_wait_ns(&ms.k_full[kb], (j >> 1) & 1, kWaitNs);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t bq = smem_u32(sQ) + (kByRows ? s * (NS / 8) * qsbo : 0);
-          const int steps = kcols / 16;
-          for (int k = 0; k < steps; ++k)
-            umma_f16_ts(tbase + kS0 + 64 * s, tbase + 128 * kb + 8 * k, umma_desc(bq + 256 * k, 128, qsbo),
-                        umma_idesc_f16(128, NS), k > 0);
+          const uint64_t bq = q_desc + (kByRows ? s * (NS / 8) * (qsbo >> 4) : 0);
+          const uint32_t d = tbase + kS0 + 64 * s, ak = tbase + 128 * kb;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) umma_f16_ts(d, ak + 8 * k, bq + 16 * k, umma_idesc_f16(128, NS), k > 0);
+          if (prod) {
+#pragma unroll
+            for (int k = 8; k < 16; ++k) umma_f16_ts(d, ak + 8 * k, bq + 16 * k, umma_idesc_f16(128, NS), 1);
+          }
           umma_commit(&ms.s_full[s]);
           if (!kByRows || s == 1) umma_commit(&ms.k_empty[kb]);
         }
@@ -521,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           if (ok) ok = mbar_wait_ns(&ms.p_full[s], i & 1, kWaitNs);
           if (!ok) break;
           tc_fence_after();
+          const uint64_t av = v_desc + vb * (kVBytes >> 4), bp = p_desc + s * (p_bytes(N) >> 4);
+#pragma unroll
           for (int k = 0; k < 8; ++k)
-            umma_f16(tbase + kO0 + 64 * s, umma_desc(smem_u32(sV) + vb * kVBytes + 256 * k, 128, 2048),
-                     umma_desc(smem_u32(sP) + s * p_bytes(N) + 256 * k, 128, 2048),
-                     umma_idesc_f16(128, NS) | kMnMajorAB, i > 0 || k > 0);
+            umma_f16(tbase + kO0 + 64 * s, av + 16 * k, bp + 16 * k, umma_idesc_f16(128, NS) | kMnMajorAB, i > 0 || k > 0);
           umma_commit(&ms.p_empty[s]);
           if (!kByRows || s == 1) umma_commit(&ms.v_empty[vb]);
         }
