@@ -163,7 +163,7 @@ __device__ __forceinline__ void key_unit(const uint32_t* w, const Levels& lv, __
 template <int BITS>
 __device__ __forceinline__ void key_row(const uint8_t* row, const Levels& lv, uint32_t tcol) {
   constexpr int WU = 16 / level_pairs(BITS);
-#pragma unroll
+#pragma unroll 1
   for (int u = 0; u < 4; ++u) {
     uint32_t w[WU];
     if constexpr (WU == 4) {
@@ -181,6 +181,7 @@ __device__ __forceinline__ void key_row(const uint8_t* row, const Levels& lv, ui
 template <int BITS>
 __device__ __forceinline__ void key_group(const uint8_t* row, int units, const Levels& lv, __half2 g, uint32_t tcol) {
   constexpr int WU = 16 / level_pairs(BITS);
+#pragma unroll 1
   for (int u = 0; u < units; ++u) {
     uint32_t w[WU];
 #pragma unroll
@@ -220,10 +221,29 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, F f) {
   return f(v[0], __shfl_xor_sync(kFull, v[0], 1));
 }
 
+// Store channels 4 lane .. 4 lane + 3 of query row `row` (token-major, then the group's heads), times f.
+__device__ __forceinline__ void store_row(const ExtendArgs& a, int b, int head0, int group, int row, int lane, float4 v,
+                                          float f) {
+  const int t = row / group, h = a.heads.head[head0 + row - t * group];
+  const int64_t at = b * a.ob + h * a.oh + t * a.ot + 4 * lane;
+  v.x *= f; v.y *= f; v.z *= f; v.w *= f;
+  if (a.out_dtype == TQ_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
+  } else if (a.out_dtype == TQ_BF16) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+        make_uint2(h2bits(__floats2half2_rn(v.x, v.y)), h2bits(__floats2half2_rn(v.z, v.w)));
+  }
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ ExtendArgs a) {
   constexpr int NS = stream_rows(N);          // rows of a stream
   constexpr bool kByRows = N > 64;            // streams split the rows (else the tiles)
+  constexpr bool kHold = NS <= 32;            // a token's logits stay in registers
   constexpr uint32_t kS0 = 256, kO0 = 384;    // tensor-memory columns: K' 0..255, S^T, O^T
 
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -314,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     const Levels lv0 = load_levels(a.tab, 0), lv1 = load_levels(a.tab, 1);
     const int tok = tid;
     const int o_sgn = kTile * a.idx_bytes, o_nrm = o_sgn + kTile * a.sgn_bytes;
+#pragma unroll 1
     for (int j = 0; j < nt; ++j) {
       const int st = j % a.stages, kb = j & 1;
       const uint8_t* raw = sRaw + st * a.stage_bytes;
@@ -352,13 +373,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           const float n16 = half_lo(nn);
           const uint32_t rho = h2bits(__float2half2_rn(n16 > 0.f ? half_hi(nn) / n16 * a.sketch_ratio : 0.f));
           scal = n16 * a.key_scale0;
-          const uint4 sg = *reinterpret_cast<const uint4*>(raw + o_sgn + 16 * tok);
-          const uint32_t inv[4] = {~sg.x, ~sg.y, ~sg.z, ~sg.w};
-#pragma unroll
+          const uint32_t* sg = reinterpret_cast<const uint32_t*>(raw + o_sgn + 16 * tok);
+#pragma unroll 1
           for (int u = 0; u < 4; ++u) {
             uint32_t r[16];
+            const uint32_t inv = ~sg[u];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = sign_level(inv[u], i, rho);
+            for (int i = 0; i < 16; ++i) r[i] = sign_level(inv, i, rho);
             tmem_st16(tk + 64 + 16 * u, r);
           }
         } else {
@@ -378,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     // ------------------------------------------------------------------ V: thread = token
     const int tok = tid - 128;
     const int o_vq = kTile * (a.idx_bytes + a.sgn_bytes + a.nrm_bytes), o_par = o_vq + kTile * a.vq_bytes;
+#pragma unroll 1
     for (int j = 0; j < nt; ++j) {
       const int st = j % a.stages, vb = j & 1;
       const uint8_t* raw = sRaw + st * a.stage_bytes;
@@ -387,16 +409,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       if (ok && j == 1 && prod) ok = mbar_wait_ns(&ms.sq_full, 0, kWaitNs);
       const int pos = ms.pos0[j & 15][tok >> 6] + (tok & 63);
       const bool there = pos < len;
-      const uint4 par = *reinterpret_cast<const uint4*>(raw + o_par + 16 * tok);
-      const uint32_t pw[4] = {par.x, par.y, par.z, par.w};
+      const uint32_t* par = reinterpret_cast<const uint32_t*>(raw + o_par + 16 * tok);
       uint8_t* dst = sV + vb * kVBytes + tok * 16;
       const uint8_t* src = raw + o_vq + tok * a.vq_bytes;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t p = there ? pw[g] : 0u;
+      // the lanes take the four groups in different orders, so that eight rows 64 (or 32) bytes
+      // apart are read from different banks
+      const int turn = a.vbits == 4 ? lane >> 1 : lane >> 2;
+#pragma unroll 1
+      for (int g0 = 0; g0 < 4; ++g0) {
+        const int g = (g0 + turn) & 3;
+        uint32_t p = there ? par[g] : 0u;
         if ((p & 0x7c00u) == 0x7c00u || (p & 0x7c000000u) == 0x7c000000u) {
-          // inf or NaN: 0 * inf would reach rows that may not see this token, so the product gets zeros and
-          // the rows that do see it are set to NaN at the end
+          // inf or NaN: 0 * inf would reach rows that may not see this token, so the product gets
+          // zeros and the rows that do see it are set to NaN at the end
           atomicMin(&ms.poison[g], pos);
           p = 0;
         }
@@ -456,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     const int off = plane == 0 ? 0 : plane == 1 ? o_sgn : plane == 2 ? o_nrm : plane == 3 ? o_vq : o_par;
     const int row_bytes = a.idx_bytes + a.sgn_bytes + a.nrm_bytes + a.vq_bytes + 16;
     int done = 0;
+#pragma unroll 1
     for (int j = 0; j < nt && ok; ++j, ++done) {
       const int st = j % a.stages;
       if (j >= a.stages) ok = mbar_wait_ns(&ms.raw_empty[st], (j / a.stages - 1) & 1, kWaitNs);
@@ -503,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         }
       }
       if (ok) ok = mbar_wait_ns(&ms.q_full, 0, kWaitNs);
+#pragma unroll 1
       for (int u = 0; u <= units && ok; ++u) {
         if (u < units) {
           const int s = u & 1, j = kByRows ? u >> 1 : u, kb = j & 1;
@@ -557,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           v[0] = half_lo(x.x); v[1] = half_hi(x.x); v[2] = half_lo(x.y); v[3] = half_hi(x.y);
         }
       };
+#pragma unroll 1
       for (int r = w8; r < rows; r += 8) {
         float v[4];
         load_row(r, v);
@@ -571,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       qscale = a.scale_log2 / down;
       const uint32_t sbits = a.tab->sign_bits[lane >> 3] >> (4 * (lane & 7));
       const float unit = down * (a.mode == TQ_MODE_GROUPED ? 0.17677669529663688f : 0.08838834764831845f);
+#pragma unroll 1
       for (int r = w8; r < N; r += 8) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (r < rows) load_row(r, v);
@@ -608,21 +637,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         tc_fence_after();
         // lane = sketch row j; a stream's warps take half of the query rows
         const int k = kD + operand_position(1, tok);
-        for (int c = 0; c < N / 2; c += 8) {
+        constexpr int kCols = N / 2 < 16 ? 16 : N / 2;   // N = 16: the first stream takes all of them
+#pragma unroll 1
+        for (int c = s * kCols; c < min(N, (s + 1) * kCols); c += 16) {
           uint32_t x[16];
-          const int n0 = s * (N / 2) + c;
-          if (c % 16 == 0 || N / 2 < 16) {
-            tmem_ld16_sync(tlane + kS0 + (N / 2 < 16 ? 0 : n0), x);
-          }
-          const int skip = N / 2 < 16 ? n0 : 0;
+          tmem_ld16_sync(tlane + kS0 + c, x);
+          uint8_t* col = sQ + (c >> 3) * 16 * kcols + (k >> 3) * 128 + (k & 7) * 2;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int n = N / 2 < 16 ? i : n0 + i;
-            if (N / 2 < 16 && (i < skip || i >= skip + 8)) continue;
-            *reinterpret_cast<__half*>(sQ + (n >> 3) * 16 * kcols + (n & 7) * 16 + (k >> 3) * 128 + (k & 7) * 2) =
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<__half*>(col + (i >> 3) * 16 * kcols + (i & 7) * 16) =
                 __float2half_rn(__uint_as_float(x[i]) * 0.125f);
-          }
-          if (N / 2 >= 16) c += 8;
         }
         tc_fence_before();
         fence_async_smem();
@@ -637,8 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     const int* limit = ms.limit + r_first;
     float* ref = ms.ref[s];
     const int mine = kByRows ? nt : (nt - s + 1) / 2;  // this stream's units
+    // its columns that hold rows, in chunks of 16; the products' other columns are never read
+    const int used = max(0, min(NS, ((rows + 15) & ~15) - r_first));
     const uint32_t tS = tlane + kS0 + 64 * s, tO = tlane + kO0 + 64 * s;
     const int lowest = kByRows ? row_limit(min(r_first, rows - 1)) : low;
+#pragma unroll 1
     for (int i = 0; i < mine; ++i) {
       const int j = kByRows ? i : 2 * i + s;
       if (ok) ok = mbar_wait_ns(&ms.s_full[s], i & 1, kWaitNs);
@@ -646,14 +673,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       const float sc = ms.scal[j & 3][tok] * qscale;
       const int pos = ms.pos0[j & 15][tok >> 6] + (tok & 63);
       const bool masked = __any_sync(kFull, pos >= lowest);
-      bool waited = i == 0;
-      // logits (base 2) of 16 rows, masked ones -inf, relative to base
-      auto logits = [&](int c, bool rel, float (&x)[16]) {
+      // logits (base 2) of 16 rows less their references; masked ones -inf
+      auto logits = [&](int c, const float* less, float* x) {
         uint32_t y[16];
         tmem_ld16_sync(tS + c, y);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float4 m4 = rel ? *reinterpret_cast<const float4*>(ref + c + 4 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 m4 = less ? *reinterpret_cast<const float4*>(less + c + 4 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
           x[4 * q] = fmaf(__uint_as_float(y[4 * q]), sc, -m4.x);
           x[4 * q + 1] = fmaf(__uint_as_float(y[4 * q + 1]), sc, -m4.y);
           x[4 * q + 2] = fmaf(__uint_as_float(y[4 * q + 2]), sc, -m4.z);
@@ -670,41 +696,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           }
         }
       };
-      float mx = -INFINITY;
+      // up to 32 rows the logits stay in registers between the check and the exponentials; 64 do
+      // not fit beside their sums and are read from tensor memory twice
+      float x[kHold ? NS : 16];
+      auto largest = [&]() {
+        float mx = -INFINITY;
+        if constexpr (kHold) {
 #pragma unroll
-      for (int c = 0; c < NS; c += 16) {
-        float x[16];
-        logits(c, true, x);
+          for (int c = 0; c < NS; c += 16) logits(c, ref, x + c);
 #pragma unroll
-        for (int q = 0; q < 16; ++q) mx = fmaxf(mx, x[q]);
-      }
-      if (named_any(1 + s, mx > kTau)) {
+          for (int q = 0; q < NS; ++q) mx = fmaxf(mx, x[q]);
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < used; c += 16) {
+            logits(c, ref, x);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) mx = fmaxf(mx, x[q]);
+          }
+        }
+        return mx;
+      };
+      bool waited = i == 0;
+      if (named_any(1 + s, largest() > kTau)) {
         // raise the references to the tile's maxima
         if (!waited && ok) ok = mbar_wait_ns(&ms.p_empty[s], (i - 1) & 1, kWaitNs);
         waited = true;
         tc_fence_after();
         float* wmax = reinterpret_cast<float*>(myP);   // free: the last product has read it
-#pragma unroll
-        for (int c = 0; c < NS; c += 16) {
-          float x[16];
-          logits(c, false, x);
-          const float m = reduce16(x, lane, [](float p, float q) { return fmaxf(p, q); });
+        float* fac = ms.fac[s];
+#pragma unroll 1
+        for (int c = 0; c < used; c += 16) {
+          float y[16];
+          logits(c, nullptr, y);
+          const float m = reduce16(y, lane, [](float p, float q) { return fmaxf(p, q); });
           if ((lane & 1) == 0) wmax[(warp & 3) * NS + c + (lane >> 1)] = m;
         }
         named_sync(1 + s, 128);
-        if (tok < NS) {
+        if (tok < used) {
           const float old = ref[tok];
           const float m = fmaxf(fmaxf(old, fmaxf(wmax[tok], wmax[NS + tok])), fmaxf(wmax[2 * NS + tok], wmax[3 * NS + tok]));
-          ms.fac[s][tok] = old == m ? 1.f : ex2(old - m);
+          fac[tok] = old == m ? 1.f : ex2(old - m);
           ref[tok] = m;
         }
         named_sync(1 + s, 128);
-        const float* fac = ms.fac[s];
 #pragma unroll
         for (int c = 0; c < NS; ++c) sum[c] *= fac[c];
         if (i > 0) {
-#pragma unroll
-          for (int c = 0; c < NS; c += 16) {
+#pragma unroll 1
+          for (int c = 0; c < used; c += 16) {
             uint32_t o[16];
             tmem_ld16_sync(tO + c, o);
 #pragma unroll
@@ -713,20 +752,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           }
           tmem_st_wait();
         }
+        if constexpr (kHold) largest();
       }
       if (!waited && ok) ok = mbar_wait_ns(&ms.p_empty[s], (i - 1) & 1, kWaitNs);
 #pragma unroll
       for (int c = 0; c < NS; c += 16) {
-        float x[16];
-        logits(c, true, x);
+        if (!kHold) {
+          if (c >= used) break;
+          logits(c, ref, x);
+        }
+        float* xc = x + (kHold ? c : 0);
         uint32_t p[8];
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          x[q] = ex2(x[q]);
-          sum[c + q] += x[q];
+          xc[q] = ex2(xc[q]);
+          sum[c + q] += xc[q];
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) p[q] = h2bits(__floats2half2_rn(x[2 * q], x[2 * q + 1]));
+        for (int q = 0; q < 8; ++q) p[q] = h2bits(__floats2half2_rn(xc[2 * q], xc[2 * q + 1]));
         *reinterpret_cast<uint4*>(myP + (c >> 3) * 2048 + tok * 16) = make_uint4(p[0], p[1], p[2], p[3]);
         *reinterpret_cast<uint4*>(myP + ((c >> 3) + 1) * 2048 + tok * 16) = make_uint4(p[4], p[5], p[6], p[7]);
       }
@@ -741,73 +784,65 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     float* wsum = reinterpret_cast<float*>(myP);
 #pragma unroll
     for (int c = 0; c < NS; c += 16) {
-      float x[16];
+      float y[16];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) x[q] = sum[c + q];
-      const float t = reduce16(x, lane, [](float p, float q) { return p + q; });
+      for (int q = 0; q < 16; ++q) y[q] = sum[c + q];
+      const float t = reduce16(y, lane, [](float p, float q) { return p + q; });
       if ((lane & 1) == 0) wsum[(warp & 3) * NS + c + (lane >> 1)] = t;
     }
     named_sync(3, 256);
-    // factors of the two streams and the joint maximum and sum (by rows: of this stream alone)
-    float* join = reinterpret_cast<float*>(&ms.scal[0][0]);   // [stream][64] factor, then m and l: free now
+    // per row: its streams' factors, the joint maximum and sum (by rows: of the row's stream alone)
+    float* fac0 = &ms.scal[0][0];   // free now: two factors, maximum and sum of 128 rows
+    float *fac1 = fac0 + kTile, *jm = fac0 + 2 * kTile, *jl = fac0 + 3 * kTile;
     if (tok < NS) {
-      const float* w0 = reinterpret_cast<float*>(sP);
-      const float* w1 = reinterpret_cast<float*>(sP + p_bytes(N));
-      const float l0 = (w0[tok] + w0[NS + tok]) + (w0[2 * NS + tok] + w0[3 * NS + tok]);
-      const float l1 = (w1[tok] + w1[NS + tok]) + (w1[2 * NS + tok] + w1[3 * NS + tok]);
+      const float* w0 = reinterpret_cast<float*>(sP) + tok;
+      const float* w1 = reinterpret_cast<float*>(sP + p_bytes(N)) + tok;
+      const float l0 = (w0[0] + w0[NS]) + (w0[2 * NS] + w0[3 * NS]);
+      const float l1 = (w1[0] + w1[NS]) + (w1[2 * NS] + w1[3 * NS]);
       if (kByRows) {
-        join[128 + s * 64 + tok] = ref[tok];
-        join[256 + s * 64 + tok] = s ? l1 : l0;
-        join[s * 64 + tok] = 1.f;
+        jm[r_first + tok] = ref[tok];
+        jl[r_first + tok] = s ? l1 : l0;
       } else if (s == 0) {
         const float m0 = ms.ref[0][tok], m1 = ms.ref[1][tok], m = fmaxf(m0, m1);
         const float f0 = m0 == m ? 1.f : ex2(m0 - m), f1 = m1 == m ? 1.f : ex2(m1 - m);
-        join[tok] = f0;
-        join[64 + tok] = f1;
-        join[128 + tok] = m;
-        join[256 + tok] = l0 * f0 + l1 * f1;
+        fac0[tok] = f0;
+        fac1[tok] = f1;
+        jm[tok] = m;
+        jl[tok] = l0 * f0 + l1 * f1;
       }
     }
     named_sync(3, 256);
-    float* xbuf = reinterpret_cast<float*>(sV);   // [row][operand position], the other stream's outputs
-    const int both = kByRows ? 0 : (nt > 1);
-    if (both && s == 1) {
-#pragma unroll
-      for (int c = 0; c < NS; c += 16) {
-        uint32_t o[16];
-        tmem_ld16_sync(tO + c, o);
-#pragma unroll
-        for (int q = 0; q < 16; ++q) xbuf[(c + q) * kD + tok] = __uint_as_float(o[q]) * join[64 + c + q];
-      }
-    }
-    if (both) named_sync(3, 256);
-    if (kByRows || s == 0) {
-      const int ch = value_channel(a.vbits, tok);
-      const int poison = ms.poison[ch >> 5];
-#pragma unroll
-      for (int c = 0; c < NS; c += 16) {
+    float* xbuf = reinterpret_cast<float*>(sV) + r_first * kD + value_channel(a.vbits, tok);   // [row][channel]
+    const bool both = !kByRows && nt > 1;
+    if (kByRows || both || s == 0) {
+      const float* f = s ? fac1 : fac0;
+      if (both && s == 0) named_sync(3, 256);   // the second stream's outputs first
+#pragma unroll 1
+      for (int c = 0; c < used; c += 16) {
         uint32_t o[16];
         tmem_ld16_sync(tO + c, o);
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          const int r = r_first + c + q;
-          if (r >= rows) continue;
-          float v = __uint_as_float(o[q]) * join[r_first + c + q];
-          if (both) v += xbuf[(c + q) * kD + tok];
-          const float l = join[256 + r_first + c + q];
-          if (poison < ms.limit[r]) v = __uint_as_float(0x7fffffffu);
-          if (n_splits == 1) {
-            const int t = (row0 + r) / group, h = a.heads.head[head0 + (row0 + r) - t * group];
-            store_element(a.out, a.out_dtype, b * a.ob + h * a.oh + t * a.ot + ch, l == 0.f ? 0.f : v / l);
-          } else {
-            float* rec = a.part + (static_cast<int64_t>(blockIdx.x) * N + r) * kPartFloats;
-            rec[4 + ch] = v;
-            if (tok == 0) {
-              rec[0] = join[128 + r];
-              rec[1] = l;
-            }
-          }
+          float v = __uint_as_float(o[q]);
+          if (!kByRows) v *= f[c + q];
+          if (both && s == 0) v += xbuf[(c + q) * kD];
+          xbuf[(c + q) * kD] = v;
         }
+      }
+      if (both && s == 1) named_sync(3, 256);
+    }
+    named_sync(3, 256);
+#pragma unroll 1
+    for (int r = warp - 8; r < rows; r += 8) {
+      float4 v = reinterpret_cast<const float4*>(sV)[r * (kD / 4) + lane];
+      if (ms.poison[lane >> 3] < ms.limit[r]) v.x = v.y = v.z = v.w = __uint_as_float(0x7fffffffu);
+      const float l = jl[r];
+      if (n_splits == 1) {
+        store_row(a, b, head0, group, row0 + r, lane, v, l == 0.f ? 0.f : 1.f / l);
+      } else {
+        float* rec = a.part + (static_cast<int64_t>(blockIdx.x) * N + r) * kPartFloats;
+        reinterpret_cast<float4*>(rec + 4)[lane] = v;
+        if (lane == 0) *reinterpret_cast<float2*>(rec) = make_float2(jm[r], l);
       }
     }
   }
@@ -815,15 +850,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   if (!ok) atomicOr(a.err, 1);
   __syncwarp();
   tc_fence_before();
-  if (nt == 0 && tid >= 256 && tid < 384) {   // no tokens: zeros, or an empty record
-    const int ch = tid - 256;
-    for (int r = 0; r < rows; ++r) {
-      if (n_splits == 1) {
-        const int t = (row0 + r) / group, h = a.heads.head[head0 + (row0 + r) - t * group];
-        store_element(a.out, a.out_dtype, b * a.ob + h * a.oh + t * a.ot + ch, 0.f);
-      } else if (ch < 2) {
-        a.part[(static_cast<int64_t>(blockIdx.x) * N + r) * kPartFloats + ch] = ch ? 0.f : kNoRef;
-      }
+  if (nt == 0) {   // no tokens: zeros, or an empty record
+#pragma unroll 1
+    for (int r = warp; r < rows; r += kWarpsAll) {
+      if (n_splits == 1)
+        store_row(a, b, head0, group, row0 + r, lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+      else if (lane == 0)
+        *reinterpret_cast<float2*>(a.part + (static_cast<int64_t>(blockIdx.x) * N + r) * kPartFloats) = make_float2(kNoRef, 0.f);
     }
   }
   if (n_splits > 1) __threadfence();
@@ -844,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   __syncthreads();
   if (!ms.last) return;
   __threadfence();
+#pragma unroll 1
   for (int r = warp; r < rows; r += kWarpsAll) {
     const float* rec = a.part + (static_cast<int64_t>(first) * N + r) * kPartFloats;
     constexpr int64_t step = static_cast<int64_t>(N) * kPartFloats;
@@ -852,6 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     M = warp_max(M);
     float L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int i0 = 0; i0 < n_splits; i0 += 4) {
       float m[4], l[4];
       float4 o[4];
@@ -873,13 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         O.z = fmaf(f, o[i].z, O.z); O.w = fmaf(f, o[i].w, O.w);
       }
     }
-    const int t = (row0 + r) / group, h = a.heads.head[head0 + (row0 + r) - t * group];
-    const int64_t at = b * a.ob + h * a.oh + t * a.ot + 4 * lane;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    store_element(a.out, a.out_dtype, at, O.x * inv);
-    store_element(a.out, a.out_dtype, at + 1, O.y * inv);
-    store_element(a.out, a.out_dtype, at + 2, O.z * inv);
-    store_element(a.out, a.out_dtype, at + 3, O.w * inv);
+    store_row(a, b, head0, group, row0 + r, lane, O, L == 0.f ? 0.f : 1.f / L);
   }
 }
 
