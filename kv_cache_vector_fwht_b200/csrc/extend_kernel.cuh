@@ -43,7 +43,7 @@ namespace tq {
 namespace ext {
 
 constexpr int kTile = 128;              // tokens of a tile
-constexpr int kThreads = 576;           // 18 warps
+constexpr int kThreads = 640;           // 20 warps: 4 K, 4 V, 8 softmax, MMA, loader, 2 to fill their warpgroup
 constexpr int kWarpsAll = kThreads / 32;
 constexpr int kMaxStages = 6;
 constexpr int kMaxList = 64;            // sequences whose block counts are listed one by one
@@ -116,6 +116,11 @@ __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cas
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
+// Registers a thread of this warpgroup may use from here on.
+template <int R>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R)); }
 // Barrier of a stream's 128 threads that tells each whether any of them asked.
 __device__ __forceinline__ bool named_any(int id, bool ask) {
   uint32_t r;
@@ -147,48 +152,35 @@ __device__ __forceinline__ int operand_position(int bits, int c) {
   return c;
 }
 
-// Unpack 32 channels (WU index words) to 16 operand pairs; SCALED: times g.
-template <int BITS, bool SCALED>
-__device__ __forceinline__ void key_unit(const uint32_t* w, const Levels& lv, __half2 g, uint32_t tcol) {
-  uint32_t r[16];
-  constexpr int NP = level_pairs(BITS), WU = 16 / NP;
+// Unpack the index words of 32 U channels to 16 U operand pairs in tensor memory; SCALED: times g.
+// All words are loaded first: the unpacking then runs without waiting for shared memory.
+template <int BITS, int U, bool SCALED>
+__device__ __forceinline__ void key_units(const uint8_t* row, const Levels& lv, __half2 g, uint32_t tcol) {
+  constexpr int NP = level_pairs(BITS), WU = 16 / NP;   // pairs of a word, words of 32 channels
+  uint32_t w[U * WU];
+  if constexpr (!SCALED && U * WU % 4 == 0) {   // rows of 16, 32 or 64 bytes; grouped rows are aligned to words
 #pragma unroll
-  for (int i = 0; i < WU; ++i) unpack_levels<BITS>(w[i], lv, *reinterpret_cast<uint32_t(*)[NP]>(r + NP * i));
-  if constexpr (SCALED) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = h2bits(__hmul2(bits_h2(r[i]), g));
-  }
-  tmem_st16(tcol, r);
-}
-template <int BITS>
-__device__ __forceinline__ void key_row(const uint8_t* row, const Levels& lv, uint32_t tcol) {
-  constexpr int WU = 16 / level_pairs(BITS);
-#pragma unroll 1
-  for (int u = 0; u < 4; ++u) {
-    uint32_t w[WU];
-    if constexpr (WU == 4) {
-      const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * u);
-      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    } else if constexpr (WU == 2) {
-      const uint2 x = *reinterpret_cast<const uint2*>(row + 8 * u);
-      w[0] = x.x; w[1] = x.y;
-    } else {
-      w[0] = *reinterpret_cast<const uint32_t*>(row + 4 * u);
+    for (int i = 0; i < U * WU / 4; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * i);
+      w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
     }
-    key_unit<BITS, false>(w, lv, __half2{}, tcol + 16 * u);
-  }
-}
-template <int BITS>
-__device__ __forceinline__ void key_group(const uint8_t* row, int units, const Levels& lv, __half2 g, uint32_t tcol) {
-  constexpr int WU = 16 / level_pairs(BITS);
-#pragma unroll 1
-  for (int u = 0; u < units; ++u) {
-    uint32_t w[WU];
+  } else {
 #pragma unroll
-    for (int i = 0; i < WU; ++i) w[i] = reinterpret_cast<const uint32_t*>(row)[WU * u + i];
-    key_unit<BITS, true>(w, lv, g, tcol + 16 * u);
+    for (int i = 0; i < U * WU; ++i) w[i] = reinterpret_cast<const uint32_t*>(row)[i];
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < WU; ++i) unpack_levels<BITS>(w[WU * u + i], lv, *reinterpret_cast<uint32_t(*)[NP]>(r + NP * i));
+    if constexpr (SCALED) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r[i] = h2bits(__hmul2(bits_h2(r[i]), g));
+    }
+    tmem_st16(tcol + 16 * u, r);
   }
 }
+
 // Channel of operand position m of V^T: chunks of 8 positions, pairs (code i, code i + 4) of a
 // word of 4-bit codes, (code i, code i + 8) of 2-bit ones.
 __device__ __forceinline__ int value_channel(int vbits, int m) {
@@ -243,7 +235,6 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ ExtendArgs a) {
   constexpr int NS = stream_rows(N);          // rows of a stream
   constexpr bool kByRows = N > 64;            // streams split the rows (else the tiles)
-  constexpr bool kHold = NS <= 32;            // a token's logits stay in registers
   constexpr uint32_t kS0 = 256, kO0 = 384;    // tensor-memory columns: K' 0..255, S^T, O^T
 
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -327,9 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   const int units = kByRows ? 2 * nt : nt;
   bool ok = true;
 
-  if (nt == 0) {
-    // nothing to attend to
-  } else if (warp < 4) {
+  // Registers move from the unpacking and issuing warpgroups to the softmax ones, whose threads hold
+  // 64 logits and 64 sums: 256 x 72 + 256 x 144 + 128 x 40 = 60416 of the launch's 640 x 96 = 61440.
+  // A warpgroup changes its share once: what follows the roles is done by the softmax warps.
+  if (warp < 4) {
+    reg_dec<72>();
     // ------------------------------------------------------------------ K: thread = token
     const Levels lv0 = load_levels(a.tab, 0), lv1 = load_levels(a.tab, 1);
     const int tok = tid;
@@ -352,34 +345,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         const __half2 g0 = __float2half2_rn(s0 * inv), g1 = __float2half2_rn(s1 * inv);
         const uint8_t* rest = row + 4 * storage_width_c(a.bits0);
         if (a.bits1 == 1) {
-          key_group<2>(row, 1, lv0, g0, tk);
-          key_group<1>(rest, 3, lv1, g1, tk + 16);
+          key_units<2, 1, true>(row, lv0, g0, tk);
+          key_units<1, 3, true>(rest, lv1, g1, tk + 16);
         } else if (a.bits1 == 2) {
-          key_group<3>(row, 1, lv0, g0, tk);
-          key_group<2>(rest, 3, lv1, g1, tk + 16);
+          key_units<3, 1, true>(row, lv0, g0, tk);
+          key_units<2, 3, true>(rest, lv1, g1, tk + 16);
         } else {
-          key_group<4>(row, 1, lv0, g0, tk);
-          key_group<3>(rest, 3, lv1, g1, tk + 16);
+          key_units<4, 1, true>(row, lv0, g0, tk);
+          key_units<3, 3, true>(rest, lv1, g1, tk + 16);
         }
       } else {
         switch (a.bits0) {
-          case 1: key_row<1>(row, lv0, tk); break;
-          case 2: key_row<2>(row, lv0, tk); break;
-          case 3: key_row<3>(row, lv0, tk); break;
-          default: key_row<4>(row, lv0, tk); break;
+          case 1: key_units<1, 4, false>(row, lv0, __half2{}, tk); break;
+          case 2: key_units<2, 4, false>(row, lv0, __half2{}, tk); break;
+          case 3: key_units<3, 4, false>(row, lv0, __half2{}, tk); break;
+          default: key_units<4, 4, false>(row, lv0, __half2{}, tk); break;
         }
         if (prod) {
           const uint32_t nn = *reinterpret_cast<const uint32_t*>(raw + o_nrm + 4 * tok);
           const float n16 = half_lo(nn);
           const uint32_t rho = h2bits(__float2half2_rn(n16 > 0.f ? half_hi(nn) / n16 * a.sketch_ratio : 0.f));
           scal = n16 * a.key_scale0;
-          const uint32_t* sg = reinterpret_cast<const uint32_t*>(raw + o_sgn + 16 * tok);
-#pragma unroll 1
+          const uint4 sg = *reinterpret_cast<const uint4*>(raw + o_sgn + 16 * tok);
+          const uint32_t inv[4] = {~sg.x, ~sg.y, ~sg.z, ~sg.w};
+#pragma unroll
           for (int u = 0; u < 4; ++u) {
             uint32_t r[16];
-            const uint32_t inv = ~sg[u];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = sign_level(inv, i, rho);
+            for (int i = 0; i < 16; ++i) r[i] = sign_level(inv[u], i, rho);
             tmem_st16(tk + 64 + 16 * u, r);
           }
         } else {
@@ -396,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       }
     }
   } else if (warp < 8) {
+    reg_dec<72>();
     // ------------------------------------------------------------------ V: thread = token
     const int tok = tid - 128;
     const int o_vq = kTile * (a.idx_bytes + a.sgn_bytes + a.nrm_bytes), o_par = o_vq + kTile * a.vq_bytes;
@@ -415,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       // the lanes take the four groups in different orders, so that eight rows 64 (or 32) bytes
       // apart are read from different banks
       const int turn = a.vbits == 4 ? lane >> 1 : lane >> 2;
-#pragma unroll 1
+#pragma unroll 2
       for (int g0 = 0; g0 < 4; ++g0) {
         const int g = (g0 + turn) & 3;
         uint32_t p = there ? par[g] : 0u;
@@ -466,9 +460,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         mbar_arrive(&ms.v_full[vb]);
       }
     }
-  } else if (warp == 17) {
+  } else if (warp >= 16) {
+    reg_dec<40>();
+    if (warp == 17) {
     // ------------------------------------------------------------------ loader
-    if (prod && lane == 0) {
+    if (prod && nt > 0 && lane == 0) {
       mbar_expect_tx(&ms.rot, kD * kD * 2);
       bulk_g2s(sV + kVBytes, a.tab->s_umma, kD * kD * 2, &ms.rot);
     }
@@ -510,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     // if another role gave up, wait here for the copies that nothing else will wait for
     for (int j = max(0, done - a.stages); j < done; ++j)
       mbar_wait_ns(&ms.raw_full[j % a.stages], (j / a.stages) & 1, kWaitNs);
-  } else if (warp == 16) {
+    } else if (warp == 16 && nt > 0) {
     // ------------------------------------------------------------------ MMA
     if (elect_one()) {
       const uint32_t qsbo = 16u * kcols;   // bytes of 8 query rows
@@ -562,12 +558,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         }
       }
     }
+    }
   } else {
     // ------------------------------------------------------------------ softmax streams
+    reg_inc<144>();
     const int s = (warp - 8) >> 2, tok = (warp & 3) * 32 + lane;
     uint8_t* myP = sP + s * p_bytes(N);
-    float qscale;
-    {  // ---- the query operand: rotated rows, and S q for prod; 8 warps
+    float qscale = 1.f;
+    if (nt > 0) {  // ---- the query operand: rotated rows, and S q for prod; 8 warps
       const int w8 = warp - 8;
       auto load_row = [&](int r, float (&v)[4]) {
         const int t = (row0 + r) / group, h = a.heads.head[head0 + (row0 + r) - t * group];
@@ -673,66 +671,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       const float sc = ms.scal[j & 3][tok] * qscale;
       const int pos = ms.pos0[j & 15][tok >> 6] + (tok & 63);
       const bool masked = __any_sync(kFull, pos >= lowest);
-      // logits (base 2) of 16 rows less their references; masked ones -inf
-      auto logits = [&](int c, const float* less, float* x) {
-        uint32_t y[16];
-        tmem_ld16_sync(tS + c, y);
+      // logits (base 2) of all rows, less their references if rel; masked ones -inf
+      float x[NS];
+      auto logits = [&](bool rel) {
+        uint32_t(&y)[NS] = reinterpret_cast<uint32_t(&)[NS]>(x);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 m4 = less ? *reinterpret_cast<const float4*>(less + c + 4 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
-          x[4 * q] = fmaf(__uint_as_float(y[4 * q]), sc, -m4.x);
-          x[4 * q + 1] = fmaf(__uint_as_float(y[4 * q + 1]), sc, -m4.y);
-          x[4 * q + 2] = fmaf(__uint_as_float(y[4 * q + 2]), sc, -m4.z);
-          x[4 * q + 3] = fmaf(__uint_as_float(y[4 * q + 3]), sc, -m4.w);
+        for (int c = 0; c < NS; c += 16) tmem_ld16(tS + c, *reinterpret_cast<uint32_t(*)[16]>(y + c));
+#pragma unroll
+        for (int c = 0; c < NS; c += 16) tmem_ld_wait_tied16(*reinterpret_cast<uint32_t(*)[16]>(y + c));
+#pragma unroll
+        for (int c = 0; c < NS; c += 4) {
+          const float4 m4 = rel ? *reinterpret_cast<const float4*>(ref + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[c] = fmaf(x[c], sc, -m4.x);
+          x[c + 1] = fmaf(x[c + 1], sc, -m4.y);
+          x[c + 2] = fmaf(x[c + 2], sc, -m4.z);
+          x[c + 3] = fmaf(x[c + 3], sc, -m4.w);
         }
         if (masked) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int4 l4 = *reinterpret_cast<const int4*>(limit + c + 4 * q);
-            x[4 * q] = pos < l4.x ? x[4 * q] : -INFINITY;
-            x[4 * q + 1] = pos < l4.y ? x[4 * q + 1] : -INFINITY;
-            x[4 * q + 2] = pos < l4.z ? x[4 * q + 2] : -INFINITY;
-            x[4 * q + 3] = pos < l4.w ? x[4 * q + 3] : -INFINITY;
+          for (int c = 0; c < NS; c += 4) {
+            const int4 l4 = *reinterpret_cast<const int4*>(limit + c);
+            x[c] = pos < l4.x ? x[c] : -INFINITY;
+            x[c + 1] = pos < l4.y ? x[c + 1] : -INFINITY;
+            x[c + 2] = pos < l4.z ? x[c + 2] : -INFINITY;
+            x[c + 3] = pos < l4.w ? x[c + 3] : -INFINITY;
           }
         }
       };
-      // up to 32 rows the logits stay in registers between the check and the exponentials; 64 do
-      // not fit beside their sums and are read from tensor memory twice
-      float x[kHold ? NS : 16];
-      auto largest = [&]() {
-        float mx = -INFINITY;
-        if constexpr (kHold) {
+      logits(true);
+      float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < NS; c += 16) logits(c, ref, x + c);
-#pragma unroll
-          for (int q = 0; q < NS; ++q) mx = fmaxf(mx, x[q]);
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < used; c += 16) {
-            logits(c, ref, x);
-#pragma unroll
-            for (int q = 0; q < 16; ++q) mx = fmaxf(mx, x[q]);
-          }
-        }
-        return mx;
-      };
+      for (int c = 0; c < NS; ++c) mx = fmaxf(mx, x[c]);
       bool waited = i == 0;
-      if (named_any(1 + s, largest() > kTau)) {
+      if (named_any(1 + s, mx > kTau)) {
         // raise the references to the tile's maxima
         if (!waited && ok) ok = mbar_wait_ns(&ms.p_empty[s], (i - 1) & 1, kWaitNs);
         waited = true;
         tc_fence_after();
         float* wmax = reinterpret_cast<float*>(myP);   // free: the last product has read it
         float* fac = ms.fac[s];
-#pragma unroll 1
-        for (int c = 0; c < used; c += 16) {
-          float y[16];
-          logits(c, nullptr, y);
-          const float m = reduce16(y, lane, [](float p, float q) { return fmaxf(p, q); });
+        logits(false);
+#pragma unroll
+        for (int c = 0; c < NS; c += 16) {
+          const float m = reduce16(*reinterpret_cast<float(*)[16]>(x + c), lane, [](float p, float q) { return fmaxf(p, q); });
           if ((lane & 1) == 0) wmax[(warp & 3) * NS + c + (lane >> 1)] = m;
         }
         named_sync(1 + s, 128);
-        if (tok < used) {
+        if (tok < NS) {
           const float old = ref[tok];
           const float m = fmaxf(fmaxf(old, fmaxf(wmax[tok], wmax[NS + tok])), fmaxf(wmax[2 * NS + tok], wmax[3 * NS + tok]));
           fac[tok] = old == m ? 1.f : ex2(old - m);
@@ -752,24 +737,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           }
           tmem_st_wait();
         }
-        if constexpr (kHold) largest();
+        logits(true);
       }
       if (!waited && ok) ok = mbar_wait_ns(&ms.p_empty[s], (i - 1) & 1, kWaitNs);
 #pragma unroll
       for (int c = 0; c < NS; c += 16) {
-        if (!kHold) {
-          if (c >= used) break;
-          logits(c, ref, x);
-        }
-        float* xc = x + (kHold ? c : 0);
         uint32_t p[8];
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          xc[q] = ex2(xc[q]);
-          sum[c + q] += xc[q];
+          x[c + q] = ex2(x[c + q]);
+          sum[c + q] += x[c + q];
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) p[q] = h2bits(__floats2half2_rn(xc[2 * q], xc[2 * q + 1]));
+        for (int q = 0; q < 8; ++q) p[q] = h2bits(__floats2half2_rn(x[c + 2 * q], x[c + 2 * q + 1]));
         *reinterpret_cast<uint4*>(myP + (c >> 3) * 2048 + tok * 16) = make_uint4(p[0], p[1], p[2], p[3]);
         *reinterpret_cast<uint4*>(myP + ((c >> 3) + 1) * 2048 + tok * 16) = make_uint4(p[4], p[5], p[6], p[7]);
       }
@@ -814,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     named_sync(3, 256);
     float* xbuf = reinterpret_cast<float*>(sV) + r_first * kD + value_channel(a.vbits, tok);   // [row][channel]
     const bool both = !kByRows && nt > 1;
-    if (kByRows || both || s == 0) {
+    if (nt > 0 && (kByRows || both || s == 0)) {
       const float* f = s ? fac1 : fac0;
       if (both && s == 0) named_sync(3, 256);   // the second stream's outputs first
 #pragma unroll 1
@@ -834,7 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     named_sync(3, 256);
 #pragma unroll 1
     for (int r = warp - 8; r < rows; r += 8) {
-      float4 v = reinterpret_cast<const float4*>(sV)[r * (kD / 4) + lane];
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);   // no tiles: zeros, or an empty record
+      if (nt > 0) v = reinterpret_cast<const float4*>(sV)[r * (kD / 4) + lane];
       if (ms.poison[lane >> 3] < ms.limit[r]) v.x = v.y = v.z = v.w = __uint_as_float(0x7fffffffu);
       const float l = jl[r];
       if (n_splits == 1) {
@@ -845,70 +826,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         if (lane == 0) *reinterpret_cast<float2*>(rec) = make_float2(jm[r], l);
       }
     }
+    if (n_splits > 1) {
+      // the last block of threads of this item joins the splits, in their order
+      const int first = blockIdx.x - split;
+      __threadfence();
+      named_sync(3, 256);
+      if (tid == 256) {
+        int* counter = a.counters + first;
+        ms.last = atomicAdd(counter, 1) == n_splits - 1;
+        if (ms.last) *counter = 0;
+      }
+      named_sync(3, 256);
+      if (ms.last) {
+        __threadfence();
+#pragma unroll 1
+        for (int r = warp - 8; r < rows; r += 8) {
+          const float* rec = a.part + (static_cast<int64_t>(first) * N + r) * kPartFloats;
+          constexpr int64_t step = static_cast<int64_t>(N) * kPartFloats;
+          float M = kNoRef;
+          for (int i = lane; i < n_splits; i += 32) M = fmaxf(M, __ldcg(rec + i * step));
+          M = warp_max(M);
+          float L = 0.f;
+          float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int i0 = 0; i0 < n_splits; i0 += 8) {
+            float2 ml[8];
+            float4 o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float* p = rec + min(i0 + i, n_splits - 1) * step;
+              ml[i] = __ldcg(reinterpret_cast<const float2*>(p));
+              o[i] = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (i0 + i >= n_splits) break;
+              const float f = ml[i].x == M ? 1.f : ex2(ml[i].x - M);
+              L = fmaf(f, ml[i].y, L);
+              O.x = fmaf(f, o[i].x, O.x); O.y = fmaf(f, o[i].y, O.y);
+              O.z = fmaf(f, o[i].z, O.z); O.w = fmaf(f, o[i].w, O.w);
+            }
+          }
+          store_row(a, b, head0, group, row0 + r, lane, O, L == 0.f ? 0.f : 1.f / L);
+        }
+      }
+    }
   }
 
   if (!ok) atomicOr(a.err, 1);
   __syncwarp();
   tc_fence_before();
-  if (nt == 0) {   // no tokens: zeros, or an empty record
-#pragma unroll 1
-    for (int r = warp; r < rows; r += kWarpsAll) {
-      if (n_splits == 1)
-        store_row(a, b, head0, group, row0 + r, lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
-      else if (lane == 0)
-        *reinterpret_cast<float2*>(a.part + (static_cast<int64_t>(blockIdx.x) * N + r) * kPartFloats) = make_float2(kNoRef, 0.f);
-    }
-  }
-  if (n_splits > 1) __threadfence();
   __syncthreads();
   if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
-  }
-  if (n_splits == 1) return;
-
-  // ---- the last block of threads of this item joins the splits, in their order
-  const int first = blockIdx.x - split;
-  if (tid == 0) {
-    int* counter = a.counters + first;
-    ms.last = atomicAdd(counter, 1) == n_splits - 1;
-    if (ms.last) *counter = 0;
-  }
-  __syncthreads();
-  if (!ms.last) return;
-  __threadfence();
-#pragma unroll 1
-  for (int r = warp; r < rows; r += kWarpsAll) {
-    const float* rec = a.part + (static_cast<int64_t>(first) * N + r) * kPartFloats;
-    constexpr int64_t step = static_cast<int64_t>(N) * kPartFloats;
-    float M = kNoRef;
-    for (int i = lane; i < n_splits; i += 32) M = fmaxf(M, __ldcg(rec + i * step));
-    M = warp_max(M);
-    float L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int i0 = 0; i0 < n_splits; i0 += 4) {
-      float m[4], l[4];
-      float4 o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i0 + i < n_splits) {
-          const float* p = rec + (i0 + i) * step;
-          m[i] = __ldcg(p);
-          l[i] = __ldcg(p + 1);
-          o[i] = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i0 + i >= n_splits || m[i] == kNoRef) continue;   // an empty record has no outputs
-        const float f = m[i] == M ? 1.f : ex2(m[i] - M);
-        L = fmaf(f, l[i], L);
-        O.x = fmaf(f, o[i].x, O.x); O.y = fmaf(f, o[i].y, O.y);
-        O.z = fmaf(f, o[i].z, O.z); O.w = fmaf(f, o[i].w, O.w);
-      }
-    }
-    store_row(a, b, head0, group, row0 + r, lane, O, L == 0.f ? 0.f : 1.f / L);
   }
 }
 
