@@ -20,7 +20,7 @@
 //                      bit arithmetic, written to tensor memory (two buffers);
 //   V (4 warps)        thread = token: v = mn16 + code s16 in fp16 (code exact, one rounding), to
 //                      shared memory (two buffers); tokens past the end are zero rows;
-//   MMA (1 thread)     issues S^T of unit u, then O^T of unit u - 1;
+//   MMA (1 thread)     issues S^T of unit u + 2, then O^T of unit u;
 //   softmax (2 x 4)    two streams: the even and the odd tiles for up to 64 rows, the lower and the
 //                      upper 64 rows beyond. Each has its own score and output columns, reference
 //                      maxima and sums, so one's exponentials run under the other's products.
@@ -318,11 +318,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   const int units = kByRows ? 2 * nt : nt;
   bool ok = true;
 
-  // Registers move from the unpacking and issuing warpgroups to the softmax ones, whose threads hold
-  // 64 logits and 64 sums: 256 x 72 + 256 x 144 + 128 x 40 = 60416 of the launch's 640 x 96 = 61440.
-  // A warpgroup changes its share once: what follows the roles is done by the softmax warps.
+  // With 64 rows a stream, registers move from the unpacking and issuing warpgroups to the softmax ones,
+  // whose threads hold 64 logits and 64 sums: 256 x 64 + 256 x 152 + 128 x 40 = 60416 of the
+  // launch's 640 x 96 = 61440. A warpgroup changes its share once (a second change would need the
+  // warpgroup synchronised in between): what follows the roles is done by the softmax warps.
+  constexpr bool kMove = NS == 64;
   if (warp < 4) {
-    reg_dec<72>();
+    if (kMove) reg_dec<64>();
     // ------------------------------------------------------------------ K: thread = token
     const Levels lv0 = load_levels(a.tab, 0), lv1 = load_levels(a.tab, 1);
     const int tok = tid;
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       }
     }
   } else if (warp < 8) {
-    reg_dec<72>();
+    if (kMove) reg_dec<64>();
     // ------------------------------------------------------------------ V: thread = token
     const int tok = tid - 128;
     const int o_vq = kTile * (a.idx_bytes + a.sgn_bytes + a.nrm_bytes), o_par = o_vq + kTile * a.vq_bytes;
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       }
     }
   } else if (warp >= 16) {
-    reg_dec<40>();
+    if (kMove) reg_dec<40>();
     if (warp == 17) {
     // ------------------------------------------------------------------ loader
     if (prod && nt > 0 && lane == 0) {
@@ -525,28 +527,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         }
       }
       if (ok) ok = mbar_wait_ns(&ms.q_full, 0, kWaitNs);
+      // S^T of unit u: its slot was read before the weights of unit u - 2 were complete
+      auto scores = [&](int u) {
+        const int s = u & 1, j = kByRows ? u >> 1 : u, kb = j & 1;
+        if (ok && (!kByRows || s == 0)) ok = mbar_wait_ns(&ms.k_full[kb], (j >> 1) & 1, kWaitNs);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t bq = q_desc + (kByRows ? s * (NS / 8) * (qsbo >> 4) : 0);
+        const uint32_t d = tbase + kS0 + 64 * s, ak = tbase + 128 * kb;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) umma_f16_ts(d, ak + 8 * k, bq + 16 * k, umma_idesc_f16(128, NS), k > 0);
+        if (prod) {
+#pragma unroll
+          for (int k = 8; k < 16; ++k) umma_f16_ts(d, ak + 8 * k, bq + 16 * k, umma_idesc_f16(128, NS), 1);
+        }
+        umma_commit(&ms.s_full[s]);
+        if (!kByRows || s == 1) umma_commit(&ms.k_empty[kb]);
+      };
+      // The scores of unit u + 2 are issued before the outputs of unit u, whose stream then waits
+      // for one product and not for two.
 #pragma unroll 1
-      for (int u = 0; u <= units && ok; ++u) {
-        if (u < units) {
-          const int s = u & 1, j = kByRows ? u >> 1 : u, kb = j & 1;
-          if (!kByRows || s == 0) ok = mbar_wait_ns(&ms.k_full[kb], (j >> 1) & 1, kWaitNs);
+      for (int u = -2; u < units && ok; ++u) {
+        const int s = u & 1, i = u >> 1, j = kByRows ? u >> 1 : u, vb = j & 1;
+        if (u >= 0) {
+          ok = mbar_wait_ns(&ms.p_full[s], i & 1, kWaitNs);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t bq = q_desc + (kByRows ? s * (NS / 8) * (qsbo >> 4) : 0);
-          const uint32_t d = tbase + kS0 + 64 * s, ak = tbase + 128 * kb;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) umma_f16_ts(d, ak + 8 * k, bq + 16 * k, umma_idesc_f16(128, NS), k > 0);
-          if (prod) {
-#pragma unroll
-            for (int k = 8; k < 16; ++k) umma_f16_ts(d, ak + 8 * k, bq + 16 * k, umma_idesc_f16(128, NS), 1);
-          }
-          umma_commit(&ms.s_full[s]);
-          if (!kByRows || s == 1) umma_commit(&ms.k_empty[kb]);
         }
-        if (u > 0) {
-          const int w = u - 1, s = w & 1, i = w >> 1, j = kByRows ? w >> 1 : w, vb = j & 1;
-          if (!kByRows || s == 0) ok = mbar_wait_ns(&ms.v_full[vb], (j >> 1) & 1, kWaitNs);
-          if (ok) ok = mbar_wait_ns(&ms.p_full[s], i & 1, kWaitNs);
+        if (u + 2 < units) scores(u + 2);
+        if (u >= 0) {
+          if (ok && (!kByRows || s == 0)) ok = mbar_wait_ns(&ms.v_full[vb], (j >> 1) & 1, kWaitNs);
           if (!ok) break;
           tc_fence_after();
           const uint64_t av = v_desc + vb * (kVBytes >> 4), bp = p_desc + s * (p_bytes(N) >> 4);
@@ -561,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     }
   } else {
     // ------------------------------------------------------------------ softmax streams
-    reg_inc<144>();
+    if (kMove) reg_inc<152>();
     const int s = (warp - 8) >> 2, tok = (warp & 3) * 32 + lane;
     uint8_t* myP = sP + s * p_bytes(N);
     float qscale = 1.f;
