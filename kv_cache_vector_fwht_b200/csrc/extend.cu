@@ -89,12 +89,18 @@ Plan plan_extend(const tq_kv_cache* c, int n_tokens, int n_select, bool listed, 
 
 template <int N>
 tq_status launch_rows(ExtendArgs& a, int blocks, cudaStream_t st) {
-  const int fixed = smem_fixed(N, a.mode == TQ_MODE_PROD ? 2 * kD : kD);
+  const int kcols = a.mode == TQ_MODE_PROD ? 2 * kD : kD;
+  // tensor memory: 384 columns of key operands for up to 32 rows a stream, 256 beyond
+  a.key_bufs = std::min(kMaxKeyBufs, (stream_rows(N) <= 32 ? 384 : 256) / (kcols / 2));
+  a.scal_ring = a.key_bufs + 2 <= 4 ? 4 : 8;
+  // a third value buffer where at least three stages of raw tiles remain
+  a.value_bufs = smem_fixed(N, kcols, 3, a.scal_ring) + 3 * a.stage_bytes <= kSmemMax ? 3 : 2;
+  const int fixed = smem_fixed(N, kcols, a.value_bufs, a.scal_ring);
   a.stages = std::min(kMaxStages, (kSmemMax - fixed) / a.stage_bytes);
   const int smem = fixed + a.stages * a.stage_bytes;
   if (cudaFuncSetAttribute(k_extend<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
     return TQ_ECUDA;
-  k_extend<N><<<blocks, kThreads, smem, st>>>(a);
+  k_extend<N><<<blocks, block_threads(N), smem, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
 }
 

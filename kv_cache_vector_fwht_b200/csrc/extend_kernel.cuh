@@ -16,17 +16,17 @@
 // One block of threads per SM works on one KV head, up to 128 query rows and a range of 128-token
 // tiles (two 64-token blocks each, listed or consecutive); its warps have roles:
 //   loader (1 warp)    packed rows of a tile to a shared ring by bulk copies, several tiles ahead;
-//   K (4 warps)        thread = token: codes to fp16 levels by byte permutes (packed.cuh), signs by
-//                      bit arithmetic, written to tensor memory (two buffers);
-//   V (4 warps)        thread = token: v = mn16 + code s16 in fp16 (code exact, one rounding), to
-//                      shared memory (two buffers); tokens past the end are zero rows;
+//   K (4 or 8 warps)   thread = token: codes to fp16 levels by byte permutes (packed.cuh), signs by
+//                      bit arithmetic, written to tensor memory (2 to 4 buffers);
+//   V (4 or 8 warps)   thread = token: v = mn16 + code s16 in fp16 (code exact, one rounding), to
+//                      shared memory (2 or 3 buffers); tokens past the end are zero rows;
 //   MMA (1 thread)     issues S^T of unit u + 2, then O^T of unit u;
 //   softmax (2 x 4)    two streams: the even and the odd tiles for up to 64 rows, the lower and the
 //                      upper 64 rows beyond. Each has its own score and output columns, reference
 //                      maxima and sums, so one's exponentials run under the other's products.
 // Softmax in base 2 relative to a reference per row that is raised only when a score exceeds
-// it by more than 8 (one vote a unit; then the stream's outputs in tensor memory and its sums
-// are scaled), so p <= 256 fits fp16. Statistics and sums in fp32. Rounded to fp16 (relative 2^-11
+// it by more than 14 (one vote a unit; then the stream's outputs in tensor memory and its sums
+// are scaled), so p <= 2^14 fits fp16. Statistics and sums in fp32. Rounded to fp16 (relative 2^-11
 // each): q', Sq' and rho, p, v; the levels are scaled by a common factor that makes them fp16
 // numbers to 2^-13 or better.
 //
@@ -43,11 +43,13 @@ namespace tq {
 namespace ext {
 
 constexpr int kTile = 128;              // tokens of a tile
-constexpr int kThreads = 640;           // 20 warps: 4 K, 4 V, 8 softmax, MMA, loader, 2 to fill their warpgroup
-constexpr int kWarpsAll = kThreads / 32;
 constexpr int kMaxStages = 6;
+constexpr int kMaxKeyBufs = 4, kMaxValueBufs = 3;
 constexpr int kMaxList = 64;            // sequences whose block counts are listed one by one
-constexpr float kTau = 8.f;             // a reference is raised when exceeded by this (base 2)
+// A reference is raised when a score exceeds it by more than this (base 2): weights reach 2^14 in fp16.
+// At 8, a tenth of the units of a 64-row stream raised (each costs three units' time); at 14 hardly
+// any but a stream's first.
+constexpr float kTau = 14.f;
 constexpr float kNoRef = -1e30f;        // reference of a row that has seen nothing
 constexpr int kNowhere = 0x40000000;    // position of a token that does not exist
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -73,7 +75,9 @@ struct ExtendArgs {
   int row_tiles;            // tiles of N query rows of the KV head with most of them
   int mode, bits0, bits1;   // code bits (grouped: outliers, then the others)
   int idx_bytes, sgn_bytes, nrm_bytes, vq_bytes, vbits;
-  int stages, stage_bytes;
+  int stages, stage_bytes;  // ring of raw tiles
+  int key_bufs, value_bufs; // operand buffers: tensor memory, shared memory
+  int scal_ring;            // tiles whose score factors are kept (a power of two >= key_bufs + 2)
   float key_scale0, key_scale1;   // level scale / sqrt(channels) of the groups
   float sketch_ratio;       // rho = sketch_ratio * r16 / n16
   float scale_log2;
@@ -86,25 +90,43 @@ struct ExtendArgs {
 // Shared-memory plan for N query rows and K columns of the key operand.
 __host__ __device__ constexpr int stream_rows(int n) { return n < 64 ? n : 64; }
 __host__ __device__ constexpr int p_bytes(int n) { return stream_rows(n) / 8 * 2048; }
+// Warpgroups that unpack keys, and as many that unpack values: two each where the softmax threads
+// leave them the registers. One warp unpacks at about 5 cycles an instruction (latencies), so a
+// decode step (N = 16) is bound by it: 131072 tokens x 8 heads took 93 us with one warpgroup each.
+__host__ __device__ constexpr int unpack_groups(int n) { return n <= 32 ? 2 : 1; }
+// K, V, 8 softmax, MMA, loader, and 2 warps that fill the last warpgroup
+__host__ __device__ constexpr int block_threads(int n) { return 32 * (8 * unpack_groups(n) + 12); }
 constexpr int kVBytes = kTile * kD * 2;
-constexpr int kMiscBytes = 4096;
-__host__ __device__ constexpr int smem_fixed(int n, int k) { return n * k * 2 + 2 * kVBytes + 2 * p_bytes(n) + kMiscBytes; }
+constexpr int kMiscBytes = 2176;
+__host__ __device__ constexpr int smem_fixed(int n, int k, int value_bufs, int scal_ring) {
+  return n * k * 2 + value_bufs * kVBytes + 2 * p_bytes(n) + kMiscBytes + scal_ring * kTile * 4;
+}
 
 struct Misc {
   uint64_t raw_full[kMaxStages], raw_empty[kMaxStages];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], p_empty[2];
+  uint64_t k_full[kMaxKeyBufs], k_empty[kMaxKeyBufs], v_full[kMaxValueBufs], v_empty[kMaxValueBufs];
+  uint64_t s_full[2], p_full[2], p_empty[2];
   uint64_t rot, sq_in, sq_full, q_full;
   uint32_t tmem;
   int last;
   int poison[4];            // per value group: lowest position of a non-finite cached value
-  unsigned qmax;            // largest finite squared norm of the rows (float bits)
+  float norm2[8];           // largest finite squared norm of each softmax warp's query rows
   int pos0[16][2];          // first position of a tile's two halves, by tile mod 16
   alignas(16) int limit[128];   // per row: positions it attends to
   alignas(16) float ref[2][64];
   alignas(16) float fac[2][64];
-  alignas(16) float scal[4][kTile];   // per token of a tile: the factor of its scores, by tile mod 4
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc fits");
+
+// Place in a ring of n, and the parity of its turn.
+struct Ring {
+  int i, turn;
+  __device__ __forceinline__ Ring(int start) : i(start), turn(0) {}
+  __device__ __forceinline__ void step(int by, int n) {
+    i += by;
+    if (i >= n) { i -= n; turn ^= 1; }
+  }
+};
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -232,19 +254,24 @@ __device__ __forceinline__ void store_row(const ExtendArgs& a, int b, int head0,
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ ExtendArgs a) {
+__global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_constant__ ExtendArgs a) {
   constexpr int NS = stream_rows(N);          // rows of a stream
   constexpr bool kByRows = N > 64;            // streams split the rows (else the tiles)
-  constexpr uint32_t kS0 = 256, kO0 = 384;    // tensor-memory columns: K' 0..255, S^T, O^T
+  constexpr int kG = unpack_groups(N);
+  constexpr int wV = 4 * kG, wS = 8 * kG, wM = wS + 8, wL = wM + 1;   // first warps of the roles
+  // tensor-memory columns: K' buffers (64 or 128 columns each), two of S^T, two of O^T
+  constexpr uint32_t kSlot = NS <= 32 ? 32 : 64, kS0 = NS <= 32 ? 384 : 256, kO0 = kS0 + 2 * kSlot;
 
   extern __shared__ __align__(1024) uint8_t smem[];
   const bool prod = a.mode == TQ_MODE_PROD;
   const int kcols = prod ? 2 * kD : kD;
+  const uint32_t kb_cols = kcols / 2;
   uint8_t* sQ = smem;
   uint8_t* sV = sQ + N * kcols * 2;
-  uint8_t* sP = sV + 2 * kVBytes;
+  uint8_t* sP = sV + a.value_bufs * kVBytes;
   Misc& ms = *reinterpret_cast<Misc*>(sP + 2 * p_bytes(N));
-  uint8_t* sRaw = reinterpret_cast<uint8_t*>(&ms) + kMiscBytes;
+  float* scal = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&ms) + kMiscBytes);   // [tile mod ring][token]
+  uint8_t* sRaw = reinterpret_cast<uint8_t*>(scal + a.scal_ring * kTile);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -279,10 +306,68 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   const int64_t pair = static_cast<int64_t>(b) * a.n_kv_heads + kv;
   const int32_t* list = a.blocks ? a.blocks + pair * a.n_select : nullptr;
   const int all_tiles = list ? (len > 0 ? (a.n_select + 1) / 2 : 0) : (top + kTile - 1) / kTile;
-  const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * split / n_splits);
-  const int nt = static_cast<int>(static_cast<int64_t>(all_tiles) * (split + 1) / n_splits) - tile0;
+  const int share = all_tiles / n_splits, more = all_tiles - share * n_splits;
+  const int tile0 = split * share + min(split, more);
+  const int nt = share + (split < more);
 
-  if (warp == 16) {
+  // The softmax warps read the query rows for the largest norm while the others set up: warp w takes
+  // rows w, w + 8, ..., up to four at a time so that their loads overlap. Up to 32 rows stay in
+  // registers. Lane l holds channels 4 l .. 4 l + 3 (grouped: in the order of the operand's groups).
+  constexpr int kRows = N / 8, kBatch = kRows < 4 ? kRows : 4;
+  constexpr bool kKeep = kRows <= 4;
+  float qv[kBatch][4] = {};
+  auto load_batch = [&](int i0) {
+    int64_t at[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {   // rows past the last repeat it
+      const int r = row0 + min((warp - wS) + 8 * (i0 + i), rows - 1), t = r / group;
+      at[i] = b * a.qb + a.heads.head[head0 + r - t * group] * a.qh + t * a.qt;
+    }
+    if (a.mode == TQ_MODE_GROUPED) {
+      const uchar4 ch = *reinterpret_cast<const uchar4*>(a.tab->chan + 4 * lane);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        qv[i][0] = load_element(a.q, a.q_dtype, at[i] + ch.x);
+        qv[i][1] = load_element(a.q, a.q_dtype, at[i] + ch.y);
+        qv[i][2] = load_element(a.q, a.q_dtype, at[i] + ch.z);
+        qv[i][3] = load_element(a.q, a.q_dtype, at[i] + ch.w);
+      }
+    } else if (a.q_dtype == TQ_F32) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) load4<true>(static_cast<const float*>(a.q) + at[i], 4 * lane, qv[i]);
+    } else {
+      uint2 x[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) x[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at[i]) + lane);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (a.q_dtype == TQ_BF16) {
+          qv[i][0] = __uint_as_float(x[i].x << 16); qv[i][1] = __uint_as_float(x[i].x & 0xffff0000u);
+          qv[i][2] = __uint_as_float(x[i].y << 16); qv[i][3] = __uint_as_float(x[i].y & 0xffff0000u);
+        } else {
+          qv[i][0] = half_lo(x[i].x); qv[i][1] = half_hi(x[i].x); qv[i][2] = half_lo(x[i].y); qv[i][3] = half_hi(x[i].y);
+        }
+      }
+    }
+  };
+  uint32_t sbits = 0;
+  if (warp >= wS && warp < wM) {
+    float top2 = 0.f;
+    sbits = a.tab->sign_bits[lane >> 3] >> (4 * (lane & 7));
+#pragma unroll 1
+    for (int i0 = 0; i0 < kRows; i0 += kBatch) {
+      load_batch(i0);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float n2 = warp_sum(qv[i][0] * qv[i][0] + qv[i][1] * qv[i][1] + qv[i][2] * qv[i][2] + qv[i][3] * qv[i][3]);
+        if (n2 < INFINITY) top2 = fmaxf(top2, n2);
+      }
+      if (8 * (i0 + kBatch) >= rows) break;
+    }
+    if (lane == 0) ms.norm2[warp - wS] = top2;
+  }
+
+  if (warp == wM) {
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
   }
@@ -291,11 +376,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       mbar_init(&ms.raw_full[i], 1);
       mbar_init(&ms.raw_empty[i], 8);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kMaxKeyBufs; ++i) {
       mbar_init(&ms.k_full[i], 4);
       mbar_init(&ms.k_empty[i], 1);
+    }
+    for (int i = 0; i < kMaxValueBufs; ++i) {
       mbar_init(&ms.v_full[i], 4);
       mbar_init(&ms.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&ms.s_full[i], 1);
       mbar_init(&ms.p_full[i], 4);
       mbar_init(&ms.p_empty[i], 1);
@@ -304,7 +393,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     mbar_init(&ms.sq_in, 8);
     mbar_init(&ms.sq_full, 1);
     mbar_init(&ms.q_full, 8);
-    ms.qmax = 0;
     fence_mbar_init();
   }
   if (tid < 4) ms.poison[tid] = 0x7fffffff;
@@ -318,32 +406,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   const int units = kByRows ? 2 * nt : nt;
   bool ok = true;
 
-  // With 64 rows a stream, registers move from the unpacking and issuing warpgroups to the softmax ones,
-  // whose threads hold 64 logits and 64 sums: 256 x 64 + 256 x 152 + 128 x 40 = 60416 of the
-  // launch's 640 x 96 = 61440. A warpgroup changes its share once (a second change would need the
-  // warpgroup synchronised in between): what follows the roles is done by the softmax warps.
-  constexpr bool kMove = NS == 64;
-  if (warp < 4) {
+  // Registers move from the unpacking and issuing warpgroups to the softmax ones, whose threads hold a
+  // logit and a sum for each of their stream's rows:
+  //   64 rows: 256 x 64 + 256 x 152 + 128 x 40 = 60416 of the launch's 640 x 96 = 61440
+  //   32 rows: 512 x 64 + 256 x 96 + 128 x 40 = 62464 of 896 x 72 = 64512
+  // A warpgroup changes its share once (a second change would need the warpgroup synchronised in
+  // between): what follows the roles is done by the softmax warps.
+  constexpr bool kMove = NS >= 32;
+  if (warp < wV) {
     if (kMove) reg_dec<64>();
     // ------------------------------------------------------------------ K: thread = token
     const Levels lv0 = load_levels(a.tab, 0), lv1 = load_levels(a.tab, 1);
-    const int tok = tid;
+    const int tok = tid & 127;
     const int o_sgn = kTile * a.idx_bytes, o_nrm = o_sgn + kTile * a.sgn_bytes;
+    Ring st(warp >> 2), kb(warp >> 2);
 #pragma unroll 1
-    for (int j = 0; j < nt; ++j) {
-      const int st = j % a.stages, kb = j & 1;
-      const uint8_t* raw = sRaw + st * a.stage_bytes;
-      if (ok) ok = mbar_wait_ns(&ms.raw_full[st], (j / a.stages) & 1, kWaitNs);
-      if (ok && j >= 2) ok = mbar_wait_ns(&ms.k_empty[kb], ((j >> 1) - 1) & 1, kWaitNs);
+    for (int j = warp >> 2; j < nt; j += kG, st.step(kG, a.stages), kb.step(kG, a.key_bufs)) {
+      const uint8_t* raw = sRaw + st.i * a.stage_bytes;
+      if (ok) ok = mbar_wait_ns(&ms.raw_full[st.i], st.turn, kWaitNs);
+      if (ok && j >= a.key_bufs) ok = mbar_wait_ns(&ms.k_empty[kb.i], kb.turn ^ 1, kWaitNs);
       tc_fence_after();
-      const uint32_t tk = tlane + 128 * kb;
+      const uint32_t tk = tlane + kb_cols * kb.i;
       const uint8_t* row = raw + tok * a.idx_bytes;
-      float scal;
+      float factor;
       if (a.mode == TQ_MODE_GROUPED) {
         const uint32_t nn = *reinterpret_cast<const uint32_t*>(raw + o_nrm + 4 * tok);
         const float s0 = half_lo(nn) * a.key_scale0, s1 = half_hi(nn) * a.key_scale1;
-        scal = fmaxf(s0, s1);
-        const float inv = scal > 0.f ? 1.f / scal : 0.f;
+        factor = fmaxf(s0, s1);
+        const float inv = factor > 0.f ? 1.f / factor : 0.f;
         const __half2 g0 = __float2half2_rn(s0 * inv), g1 = __float2half2_rn(s1 * inv);
         const uint8_t* rest = row + 4 * storage_width_c(a.bits0);
         if (a.bits1 == 1) {
@@ -367,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           const uint32_t nn = *reinterpret_cast<const uint32_t*>(raw + o_nrm + 4 * tok);
           const float n16 = half_lo(nn);
           const uint32_t rho = h2bits(__float2half2_rn(n16 > 0.f ? half_hi(nn) / n16 * a.sketch_ratio : 0.f));
-          scal = n16 * a.key_scale0;
+          factor = n16 * a.key_scale0;
           const uint4 sg = *reinterpret_cast<const uint4*>(raw + o_sgn + 16 * tok);
           const uint32_t inv[4] = {~sg.x, ~sg.y, ~sg.z, ~sg.w};
 #pragma unroll
@@ -378,35 +468,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             tmem_st16(tk + 64 + 16 * u, r);
           }
         } else {
-          scal = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(raw + o_nrm + 2 * tok))) * a.key_scale0;
+          factor = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(raw + o_nrm + 2 * tok))) * a.key_scale0;
         }
       }
-      ms.scal[j & 3][tok] = scal;
+      scal[(j & (a.scal_ring - 1)) * kTile + tok] = factor;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&ms.raw_empty[st]);
-        mbar_arrive(&ms.k_full[kb]);
+        mbar_arrive(&ms.raw_empty[st.i]);
+        mbar_arrive(&ms.k_full[kb.i]);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < wS) {
     if (kMove) reg_dec<64>();
     // ------------------------------------------------------------------ V: thread = token
-    const int tok = tid - 128;
+    const int tok = tid & 127;
     const int o_vq = kTile * (a.idx_bytes + a.sgn_bytes + a.nrm_bytes), o_par = o_vq + kTile * a.vq_bytes;
+    Ring st((warp - wV) >> 2), vb((warp - wV) >> 2);
 #pragma unroll 1
-    for (int j = 0; j < nt; ++j) {
-      const int st = j % a.stages, vb = j & 1;
-      const uint8_t* raw = sRaw + st * a.stage_bytes;
-      if (ok) ok = mbar_wait_ns(&ms.raw_full[st], (j / a.stages) & 1, kWaitNs);
-      if (ok && j >= 2) ok = mbar_wait_ns(&ms.v_empty[vb], ((j >> 1) - 1) & 1, kWaitNs);
+    for (int j = (warp - wV) >> 2; j < nt; j += kG, st.step(kG, a.stages), vb.step(kG, a.value_bufs)) {
+      const uint8_t* raw = sRaw + st.i * a.stage_bytes;
+      if (ok) ok = mbar_wait_ns(&ms.raw_full[st.i], st.turn, kWaitNs);
+      if (ok && j >= a.value_bufs) ok = mbar_wait_ns(&ms.v_empty[vb.i], vb.turn ^ 1, kWaitNs);
       // the second buffer holds the sketch matrix until S q has been formed
       if (ok && j == 1 && prod) ok = mbar_wait_ns(&ms.sq_full, 0, kWaitNs);
       const int pos = ms.pos0[j & 15][tok >> 6] + (tok & 63);
       const bool there = pos < len;
       const uint32_t* par = reinterpret_cast<const uint32_t*>(raw + o_par + 16 * tok);
-      uint8_t* dst = sV + vb * kVBytes + tok * 16;
+      uint8_t* dst = sV + vb.i * kVBytes + tok * 16;
       const uint8_t* src = raw + o_vq + tok * a.vq_bytes;
       // the lanes take the four groups in different orders, so that eight rows 64 (or 32) bytes
       // apart are read from different banks
@@ -458,13 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&ms.raw_empty[st]);
-        mbar_arrive(&ms.v_full[vb]);
+        mbar_arrive(&ms.raw_empty[st.i]);
+        mbar_arrive(&ms.v_full[vb.i]);
       }
     }
-  } else if (warp >= 16) {
+  } else if (warp >= wM) {
     if (kMove) reg_dec<40>();
-    if (warp == 17) {
+    if (warp == wL) {
     // ------------------------------------------------------------------ loader
     if (prod && nt > 0 && lane == 0) {
       mbar_expect_tx(&ms.rot, kD * kD * 2);
@@ -478,11 +568,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     const int rb = plane == 0 ? a.idx_bytes : plane == 1 ? a.sgn_bytes : plane == 2 ? a.nrm_bytes : plane == 3 ? a.vq_bytes : 16;
     const int off = plane == 0 ? 0 : plane == 1 ? o_sgn : plane == 2 ? o_nrm : plane == 3 ? o_vq : o_par;
     const int row_bytes = a.idx_bytes + a.sgn_bytes + a.nrm_bytes + a.vq_bytes + 16;
-    int done = 0;
+    int j = 0;
+    Ring ring(0);
 #pragma unroll 1
-    for (int j = 0; j < nt && ok; ++j, ++done) {
-      const int st = j % a.stages;
-      if (j >= a.stages) ok = mbar_wait_ns(&ms.raw_empty[st], (j / a.stages - 1) & 1, kWaitNs);
+    for (; j < nt; ++j, ring.step(1, a.stages)) {
+      const int st = ring.i;
+      if (j >= a.stages) ok = mbar_wait_ns(&ms.raw_empty[st], ring.turn ^ 1, kWaitNs);
       if (!ok) break;
       int p[2], n[2];
 #pragma unroll
@@ -500,15 +591,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         mbar_expect_tx(&ms.raw_full[st], (n[0] + n[1]) * row_bytes);
       }
       __syncwarp();
+      if (p[1] == p[0] + TQ_BLOCK) {   // consecutive blocks: one copy a plane (fewer, larger copies)
+        n[0] += n[1];
+        n[1] = 0;
+      }
       const int mine = half == 0 ? n[0] : n[1], from = half == 0 ? p[0] : p[1];
       if (lane < 10 && mine > 0 && rb > 0)
         bulk_g2s(sRaw + st * a.stage_bytes + off + half * TQ_BLOCK * rb,
                  base + (pair * a.capacity + from) * rb, mine * rb, &ms.raw_full[st]);
     }
     // if another role gave up, wait here for the copies that nothing else will wait for
-    for (int j = max(0, done - a.stages); j < done; ++j)
-      mbar_wait_ns(&ms.raw_full[j % a.stages], (j / a.stages) & 1, kWaitNs);
-    } else if (warp == 16 && nt > 0) {
+#pragma unroll 1
+    for (int k = max(0, j - a.stages); k < j; ++k)
+      mbar_wait_ns(&ms.raw_full[k % a.stages], (k / a.stages) & 1, kWaitNs);
+    } else if (warp == wM && nt > 0) {
     // ------------------------------------------------------------------ MMA
     if (elect_one()) {
       const uint32_t qsbo = 16u * kcols;   // bytes of 8 query rows
@@ -527,14 +623,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         }
       }
       if (ok) ok = mbar_wait_ns(&ms.q_full, 0, kWaitNs);
+      Ring kb(0), vb(0);
       // S^T of unit u: its slot was read before the weights of unit u - 2 were complete
       auto scores = [&](int u) {
-        const int s = u & 1, j = kByRows ? u >> 1 : u, kb = j & 1;
-        if (ok && (!kByRows || s == 0)) ok = mbar_wait_ns(&ms.k_full[kb], (j >> 1) & 1, kWaitNs);
+        const int s = u & 1;
+        if (ok && (!kByRows || s == 0)) ok = mbar_wait_ns(&ms.k_full[kb.i], kb.turn, kWaitNs);
         if (!ok) return;
         tc_fence_after();
         const uint64_t bq = q_desc + (kByRows ? s * (NS / 8) * (qsbo >> 4) : 0);
-        const uint32_t d = tbase + kS0 + 64 * s, ak = tbase + 128 * kb;
+        const uint32_t d = tbase + kS0 + kSlot * s, ak = tbase + kb_cols * kb.i;
 #pragma unroll
         for (int k = 0; k < 8; ++k) umma_f16_ts(d, ak + 8 * k, bq + 16 * k, umma_idesc_f16(128, NS), k > 0);
         if (prod) {
@@ -542,13 +639,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           for (int k = 8; k < 16; ++k) umma_f16_ts(d, ak + 8 * k, bq + 16 * k, umma_idesc_f16(128, NS), 1);
         }
         umma_commit(&ms.s_full[s]);
-        if (!kByRows || s == 1) umma_commit(&ms.k_empty[kb]);
+        if (!kByRows || s == 1) {   // the tile's last unit
+          umma_commit(&ms.k_empty[kb.i]);
+          kb.step(1, a.key_bufs);
+        }
       };
       // The scores of unit u + 2 are issued before the outputs of unit u, whose stream then waits
       // for one product and not for two.
 #pragma unroll 1
       for (int u = -2; u < units && ok; ++u) {
-        const int s = u & 1, i = u >> 1, j = kByRows ? u >> 1 : u, vb = j & 1;
+        const int s = u & 1, i = u >> 1;
         if (u >= 0) {
           ok = mbar_wait_ns(&ms.p_full[s], i & 1, kWaitNs);
           if (!ok) break;
@@ -556,85 +656,73 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         }
         if (u + 2 < units) scores(u + 2);
         if (u >= 0) {
-          if (ok && (!kByRows || s == 0)) ok = mbar_wait_ns(&ms.v_full[vb], (j >> 1) & 1, kWaitNs);
+          if (ok && (!kByRows || s == 0)) ok = mbar_wait_ns(&ms.v_full[vb.i], vb.turn, kWaitNs);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t av = v_desc + vb * (kVBytes >> 4), bp = p_desc + s * (p_bytes(N) >> 4);
+          const uint64_t av = v_desc + vb.i * (kVBytes >> 4), bp = p_desc + s * (p_bytes(N) >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            umma_f16(tbase + kO0 + 64 * s, av + 16 * k, bp + 16 * k, umma_idesc_f16(128, NS) | kMnMajorAB, i > 0 || k > 0);
+            umma_f16(tbase + kO0 + kSlot * s, av + 16 * k, bp + 16 * k, umma_idesc_f16(128, NS) | kMnMajorAB, i > 0 || k > 0);
           umma_commit(&ms.p_empty[s]);
-          if (!kByRows || s == 1) umma_commit(&ms.v_empty[vb]);
+          if (!kByRows || s == 1) {
+            umma_commit(&ms.v_empty[vb.i]);
+            vb.step(1, a.value_bufs);
+          }
         }
       }
     }
     }
   } else {
     // ------------------------------------------------------------------ softmax streams
-    if (kMove) reg_inc<152>();
-    const int s = (warp - 8) >> 2, tok = (warp & 3) * 32 + lane;
+    if (kMove) reg_inc<NS == 64 ? 152 : 96>();
+    const int s = (warp - wS) >> 2, tok = (warp & 3) * 32 + lane;
     uint8_t* myP = sP + s * p_bytes(N);
     float qscale = 1.f;
-    if (nt > 0) {  // ---- the query operand: rotated rows, and S q for prod; 8 warps
-      const int w8 = warp - 8;
-      auto load_row = [&](int r, float (&v)[4]) {
-        const int t = (row0 + r) / group, h = a.heads.head[head0 + (row0 + r) - t * group];
-        const int64_t at = b * a.qb + h * a.qh + t * a.qt;
-        if (a.mode == TQ_MODE_GROUPED) {
+    if (nt > 0) {  // ---- the query operand: rotated rows, and S q for prod
+      float n2 = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = load_element(a.q, a.q_dtype, at + a.tab->chan[4 * lane + i]);
-        } else if (a.q_dtype == TQ_F32) {
-          load4<true>(static_cast<const float*>(a.q) + at, 4 * lane, v);
-        } else if (a.q_dtype == TQ_BF16) {
-          load4<false>(static_cast<const uint16_t*>(a.q) + at, 4 * lane, v);
-        } else {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at) + lane);
-          v[0] = half_lo(x.x); v[1] = half_hi(x.x); v[2] = half_lo(x.y); v[3] = half_hi(x.y);
-        }
-      };
-#pragma unroll 1
-      for (int r = w8; r < rows; r += 8) {
-        float v[4];
-        load_row(r, v);
-        const float n2 = warp_sum(v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3]);
-        if (lane == 0 && n2 < INFINITY) atomicMax(&ms.qmax, __float_as_uint(n2));
-      }
-      named_sync(3, 256);
-      // a power of two that brings the longest row to a norm of 8 .. 16 (the other rows are shorter)
-      const float n2 = __uint_as_float(ms.qmax);
-      const int e = n2 > 0.f ? (ilogbf(n2) >> 1) - 3 : 0;
-      const float down = exp2f(static_cast<float>(-max(-120, min(120, e))));
-      qscale = a.scale_log2 / down;
-      const uint32_t sbits = a.tab->sign_bits[lane >> 3] >> (4 * (lane & 7));
+      for (int i = 0; i < 8; ++i) n2 = fmaxf(n2, ms.norm2[i]);
+      // a power of two that brings the longest row to a norm of 8 .. 16 (the other rows are shorter):
+      // half the exponent of its square, less three
+      const int e = max(-60, min(60, ((static_cast<int>(__float_as_uint(n2) >> 23) - 127) >> 1) - 3));
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      qscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       const float unit = down * (a.mode == TQ_MODE_GROUPED ? 0.17677669529663688f : 0.08838834764831845f);
+      const int last_stage = a.mode == TQ_MODE_GROUPED ? 4 : 16;   // grouped: 32-point blocks
 #pragma unroll 1
-      for (int r = w8; r < N; r += 8) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r < rows) load_row(r, v);
+      for (int i = 0; i < kRows; ++i) {
+        const int r = (warp - wS) + 8 * i;
+        if (!kKeep && i % kBatch == 0 && r < rows) load_batch(i);
+        float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = flip_sign(v[i] * unit, sbits, i);
+        for (int k = 0; k < 4; ++k) {
+          v[k] = qv[0][k];
+#pragma unroll
+          for (int n = 1; n < kBatch; ++n) v[k] = i % kBatch == n ? qv[n][k] : v[k];
+          v[k] = r < rows ? flip_sign(v[k] * unit, sbits, k) : 0.f;
+        }
         fwht_reg<4>(v);
+#pragma unroll 1
+        for (int m = 1; m <= last_stage; m <<= 1) {
 #pragma unroll
-        for (int m = 1; m <= 16; m <<= 1) {
-          if (m == 8 && a.mode == TQ_MODE_GROUPED) break;   // 32-point blocks
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float o = __shfl_xor_sync(kFull, v[i], m);
-            v[i] = lane & m ? o - v[i] : v[i] + o;
+          for (int k = 0; k < 4; ++k) {
+            const float o = __shfl_xor_sync(kFull, v[k], m);
+            v[k] = lane & m ? o - v[k] : v[k] + o;
           }
         }
         uint8_t* qrow = sQ + (r >> 3) * 16 * kcols + (r & 7) * 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 4 * lane + i;
-          const int k = a.mode != TQ_MODE_GROUPED ? operand_position(a.bits0, c)
-                        : c < 32                  ? operand_position(a.bits0, c)
-                                                  : 32 + operand_position(a.bits1, c - 32);
-          const __half h = __float2half_rn(v[i]);
+        uint8_t* prow = sP + (r >> 3) * 2048 + (r & 7) * 16;
+#pragma unroll 1
+        for (int k4 = 0; k4 < 4; ++k4) {
+          const int c = 4 * lane + k4;
+          const bool rest = a.mode == TQ_MODE_GROUPED && c >= 32;
+          const int k = rest ? 32 + operand_position(a.bits1, c - 32) : operand_position(a.bits0, c);
+          const __half h = __float2half_rn(v[0]);
+          v[0] = v[1]; v[1] = v[2]; v[2] = v[3];
           *reinterpret_cast<__half*>(qrow + (k >> 3) * 128 + (k & 7) * 2) = h;
-          if (prod) {
+          if (prod) {   // the sketch matrix's column order: c, c + 64 side by side
             const int k2 = c < 64 ? 2 * c : 2 * (c - 64) + 1;
-            *reinterpret_cast<__half*>(sP + (r >> 3) * 2048 + (r & 7) * 16 + (k2 >> 3) * 128 + (k2 & 7) * 2) = h;
+            *reinterpret_cast<__half*>(prow + (k2 >> 3) * 128 + (k2 & 7) * 2) = h;
           }
         }
       }
@@ -671,14 +759,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     const int mine = kByRows ? nt : (nt - s + 1) / 2;  // this stream's units
     // its columns that hold rows, in chunks of 16; the products' other columns are never read
     const int used = max(0, min(NS, ((rows + 15) & ~15) - r_first));
-    const uint32_t tS = tlane + kS0 + 64 * s, tO = tlane + kO0 + 64 * s;
+    const uint32_t tS = tlane + kS0 + kSlot * s, tO = tlane + kO0 + kSlot * s;
     const int lowest = kByRows ? row_limit(min(r_first, rows - 1)) : low;
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
       const int j = kByRows ? i : 2 * i + s;
       if (ok) ok = mbar_wait_ns(&ms.s_full[s], i & 1, kWaitNs);
       tc_fence_after();
-      const float sc = ms.scal[j & 3][tok] * qscale;
+      const float sc = scal[(j & (a.scal_ring - 1)) * kTile + tok] * qscale;
       const int pos = ms.pos0[j & 15][tok >> 6] + (tok & 63);
       const bool masked = __any_sync(kFull, pos >= lowest);
       // logits (base 2) of all rows, less their references if rel; masked ones -inf
@@ -782,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     }
     named_sync(3, 256);
     // per row: its streams' factors, the joint maximum and sum (by rows: of the row's stream alone)
-    float* fac0 = &ms.scal[0][0];   // free now: two factors, maximum and sum of 128 rows
+    float* fac0 = scal;   // free now: two factors, maximum and sum of 128 rows
     float *fac1 = fac0 + kTile, *jm = fac0 + 2 * kTile, *jl = fac0 + 3 * kTile;
     if (tok < NS) {
       const float* w0 = reinterpret_cast<float*>(sP) + tok;
@@ -822,8 +910,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       if (both && s == 1) named_sync(3, 256);
     }
     named_sync(3, 256);
-#pragma unroll 1
-    for (int r = warp - 8; r < rows; r += 8) {
+#pragma unroll 2
+    for (int r = warp - wS; r < rows; r += 8) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);   // no tiles: zeros, or an empty record
       if (nt > 0) v = reinterpret_cast<const float4*>(sV)[r * (kD / 4) + lane];
       if (ms.poison[lane >> 3] < ms.limit[r]) v.x = v.y = v.z = v.w = __uint_as_float(0x7fffffffu);
@@ -841,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       const int first = blockIdx.x - split;
       __threadfence();
       named_sync(3, 256);
-      if (tid == 256) {
+      if (tid == 32 * wS) {
         int* counter = a.counters + first;
         ms.last = atomicAdd(counter, 1) == n_splits - 1;
         if (ms.last) *counter = 0;
@@ -849,35 +937,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       named_sync(3, 256);
       if (ms.last) {
         __threadfence();
+        // records in batches of 8 loads, of four rows where there are many rows (and few splits)
+        constexpr int kRb = N >= 64 ? 4 : 1, kSb = 8 / kRb;
+        constexpr int64_t step = static_cast<int64_t>(N) * kPartFloats;
 #pragma unroll 1
-        for (int r = warp - 8; r < rows; r += 8) {
-          const float* rec = a.part + (static_cast<int64_t>(first) * N + r) * kPartFloats;
-          constexpr int64_t step = static_cast<int64_t>(N) * kPartFloats;
-          float M = kNoRef;
-          for (int i = lane; i < n_splits; i += 32) M = fmaxf(M, __ldcg(rec + i * step));
-          M = warp_max(M);
-          float L = 0.f;
-          float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-          for (int i0 = 0; i0 < n_splits; i0 += 8) {
-            float2 ml[8];
-            float4 o[8];
+        for (int r0 = warp - wS; r0 < rows; r0 += 8 * kRb) {
+          const float* rec = a.part + (static_cast<int64_t>(first) * N + r0) * kPartFloats;
+          float M[kRb], L[kRb];
+          float4 O[kRb];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float* p = rec + min(i0 + i, n_splits - 1) * step;
-              ml[i] = __ldcg(reinterpret_cast<const float2*>(p));
-              o[i] = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
+          for (int k = 0; k < kRb; ++k) { M[k] = kNoRef; L[k] = 0.f; O[k] = make_float4(0.f, 0.f, 0.f, 0.f); }
+#pragma unroll 1
+          for (int i0 = 0; i0 < n_splits; i0 += kSb) {
+            float2 ml[kRb][kSb];
+            float4 o[kRb][kSb];
+#pragma unroll
+            for (int k = 0; k < kRb; ++k) {
+              const int more_rows = min(8 * k, (rows - 1 - r0) & ~7);   // past the last row: an earlier one again
+#pragma unroll
+              for (int i = 0; i < kSb; ++i) {
+                const float* p = rec + more_rows * kPartFloats + min(i0 + i, n_splits - 1) * step;
+                ml[k][i] = __ldcg(reinterpret_cast<const float2*>(p));
+                o[k][i] = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
+              }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (i0 + i >= n_splits) break;
-              const float f = ml[i].x == M ? 1.f : ex2(ml[i].x - M);
-              L = fmaf(f, ml[i].y, L);
-              O.x = fmaf(f, o[i].x, O.x); O.y = fmaf(f, o[i].y, O.y);
-              O.z = fmaf(f, o[i].z, O.z); O.w = fmaf(f, o[i].w, O.w);
+            for (int k = 0; k < kRb; ++k) {
+              float m = M[k];
+#pragma unroll
+              for (int i = 0; i < kSb; ++i) m = fmaxf(m, ml[k][i].x);
+              const float g = M[k] == m ? 1.f : ex2(M[k] - m);
+              M[k] = m;
+              L[k] *= g;
+              O[k].x *= g; O[k].y *= g; O[k].z *= g; O[k].w *= g;
+#pragma unroll
+              for (int i = 0; i < kSb; ++i) {
+                if (i0 + i < n_splits) {
+                  const float f = ml[k][i].x == m ? 1.f : ex2(ml[k][i].x - m);
+                  L[k] = fmaf(f, ml[k][i].y, L[k]);
+                  O[k].x = fmaf(f, o[k][i].x, O[k].x); O[k].y = fmaf(f, o[k][i].y, O[k].y);
+                  O[k].z = fmaf(f, o[k][i].z, O[k].z); O[k].w = fmaf(f, o[k][i].w, O[k].w);
+                }
+              }
             }
           }
-          store_row(a, b, head0, group, row0 + r, lane, O, L == 0.f ? 0.f : 1.f / L);
+#pragma unroll
+          for (int k = 0; k < kRb; ++k)
+            if (r0 + 8 * k < rows) store_row(a, b, head0, group, row0 + r0 + 8 * k, lane, O[k], L[k] == 0.f ? 0.f : 1.f / L[k]);
         }
       }
     }
@@ -887,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == wM) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
