@@ -88,7 +88,7 @@ struct ExtendArgs {
 };
 
 // Shared-memory plan for N query rows and K columns of the key operand.
-__host__ __device__ constexpr int stream_rows(int n) { return n < 64 ? n : 64; }
+__host__ __device__ constexpr int stream_rows(int n) { return n <= 64 ? n : n / 2; }
 __host__ __device__ constexpr int p_bytes(int n) { return stream_rows(n) / 8 * 2048; }
 // Warpgroups that unpack keys, and as many that unpack values: two each where the softmax threads
 // leave them the registers. One warp unpacks at about 5 cycles an instruction (latencies), so a
@@ -113,7 +113,7 @@ struct Misc {
   float norm2[8];           // largest finite squared norm of each softmax warp's query rows
   int pos0[16][2];          // first position of a tile's two halves, by tile mod 16
   alignas(16) int limit[128];   // per row: positions it attends to
-  alignas(16) float ref[2][64];
+  alignas(16) float ref[2][64];   // negated references
   alignas(16) float fac[2][64];
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc fits");
@@ -131,6 +131,11 @@ struct Ring {
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {   // one instruction
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 __device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
   // The softmax warps read the query rows for the largest norm while the others set up: warp w takes
   // rows w, w + 8, ..., up to four at a time so that their loads overlap. Up to 32 rows stay in
   // registers. Lane l holds channels 4 l .. 4 l + 3 (grouped: in the order of the operand's groups).
-  constexpr int kRows = N / 8, kBatch = kRows < 4 ? kRows : 4;
+  constexpr int kRows = N / 8, kBatch = kRows <= 4 ? kRows : kRows % 4 == 0 ? 4 : 3;
   constexpr bool kKeep = kRows <= 4;
   float qv[kBatch][4] = {};
   auto load_batch = [&](int i0) {
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
   }
   if (tid < 4) ms.poison[tid] = 0x7fffffff;
   if (tid < N) ms.limit[tid] = tid < rows ? row_limit(tid) : 0;
-  if (tid < 128) ms.ref[tid >> 6][tid & 63] = kNoRef;
+  if (tid < 128) ms.ref[tid >> 6][tid & 63] = -kNoRef;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
 
   // Registers move from the unpacking and issuing warpgroups to the softmax ones, whose threads hold a
   // logit and a sum for each of their stream's rows:
-  //   64 rows: 256 x 64 + 256 x 152 + 128 x 40 = 60416 of the launch's 640 x 96 = 61440
+  //   48, 64 rows: 256 x 64 + 256 x 152 + 128 x 40 = 60416 of the launch's 640 x 96 = 61440
   //   32 rows: 512 x 64 + 256 x 96 + 128 x 40 = 62464 of 896 x 72 = 64512
   // A warpgroup changes its share once (a second change would need the warpgroup synchronised in
   // between): what follows the roles is done by the softmax warps.
@@ -674,7 +679,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     }
   } else {
     // ------------------------------------------------------------------ softmax streams
-    if (kMove) reg_inc<NS == 64 ? 152 : 96>();
+    if (kMove) reg_inc<NS >= 48 ? 152 : 96>();
     const int s = (warp - wS) >> 2, tok = (warp & 3) * 32 + lane;
     uint8_t* myP = sP + s * p_bytes(N);
     float qscale = 1.f;
@@ -689,40 +694,68 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       qscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       const float unit = down * (a.mode == TQ_MODE_GROUPED ? 0.17677669529663688f : 0.08838834764831845f);
       const int last_stage = a.mode == TQ_MODE_GROUPED ? 4 : 16;   // grouped: 32-point blocks
+      // kRot rows at a time: many rows for the overlap of their shuffles, one at a time (and less code to
+      // fetch) where there are few
+      constexpr int kRot = kKeep ? 1 : kBatch;
 #pragma unroll 1
-      for (int i = 0; i < kRows; ++i) {
-        const int r = (warp - wS) + 8 * i;
-        if (!kKeep && i % kBatch == 0 && r < rows) load_batch(i);
-        float v[4];
+      for (int i0 = 0; i0 < kRows; i0 += kRot) {
+        const int first = (warp - wS) + 8 * i0;
+        if (!kKeep && first < rows) load_batch(i0);
+        float v[kRot][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] = qv[0][k];
-#pragma unroll
-          for (int n = 1; n < kBatch; ++n) v[k] = i % kBatch == n ? qv[n][k] : v[k];
-          v[k] = r < rows ? flip_sign(v[k] * unit, sbits, k) : 0.f;
-        }
-        fwht_reg<4>(v);
-#pragma unroll 1
-        for (int m = 1; m <= last_stage; m <<= 1) {
+        for (int i = 0; i < kRot; ++i)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float o = __shfl_xor_sync(kFull, v[k], m);
-            v[k] = lane & m ? o - v[k] : v[k] + o;
+            v[i][k] = qv[i][k];
+#pragma unroll
+            for (int n = 1; kKeep && n < kBatch; ++n) v[i][k] = i0 == n ? qv[n][k] : v[i][k];
+            v[i][k] = flip_sign(v[i][k] * unit, sbits, k);
+          }
+        if (first < rows) {
+#pragma unroll
+          for (int i = 0; i < kRot; ++i) fwht_reg<4>(v[i]);
+#pragma unroll
+          for (int m = 1; m <= 16; m <<= 1) {
+            if (m > last_stage) break;
+#pragma unroll
+            for (int i = 0; i < kRot; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float o = __shfl_xor_sync(kFull, v[i][k], m);
+                v[i][k] = lane & m ? o - v[i][k] : v[i][k] + o;
+              }
           }
         }
-        uint8_t* qrow = sQ + (r >> 3) * 16 * kcols + (r & 7) * 16;
-        uint8_t* prow = sP + (r >> 3) * 2048 + (r & 7) * 16;
-#pragma unroll 1
-        for (int k4 = 0; k4 < 4; ++k4) {
-          const int c = 4 * lane + k4;
-          const bool rest = a.mode == TQ_MODE_GROUPED && c >= 32;
-          const int k = rest ? 32 + operand_position(a.bits1, c - 32) : operand_position(a.bits0, c);
-          const __half h = __float2half_rn(v[0]);
-          v[0] = v[1]; v[1] = v[2]; v[2] = v[3];
-          *reinterpret_cast<__half*>(qrow + (k >> 3) * 128 + (k & 7) * 2) = h;
-          if (prod) {   // the sketch matrix's column order: c, c + 64 side by side
-            const int k2 = c < 64 ? 2 * c : 2 * (c - 64) + 1;
-            *reinterpret_cast<__half*>(prow + (k2 >> 3) * 128 + (k2 & 7) * 2) = h;
+#pragma unroll
+        for (int i = 0; i < kRot; ++i) {
+          const int r = first + 8 * i;
+          uint8_t* qrow = sQ + (r >> 3) * 16 * kcols + (r & 7) * 16;
+          uint8_t* prow = sP + (r >> 3) * 2048 + (r & 7) * 16;   // in the sketch matrix's column order
+          if (r >= rows) {   // zeros: no row, no score above its reference
+            if (lane < 16) {
+              *reinterpret_cast<uint4*>(qrow + 128 * lane) = make_uint4(0, 0, 0, 0);
+              if (prod) *reinterpret_cast<uint4*>(prow + 128 * lane) = make_uint4(0, 0, 0, 0);
+            }
+            continue;
+          }
+          const uint32_t h01 = h2bits(__floats2half2_rn(v[i][0], v[i][1])), h23 = h2bits(__floats2half2_rn(v[i][2], v[i][3]));
+          if (a.mode != TQ_MODE_GROUPED && a.bits0 >= 3) {   // the operand's order is the coordinates'
+            *reinterpret_cast<uint2*>(qrow + (lane >> 1) * 128 + (lane & 1) * 8) = make_uint2(h01, h23);
+          } else {
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) {
+              const int c = 4 * lane + k4;
+              const bool rest = a.mode == TQ_MODE_GROUPED && c >= 32;
+              const int k = rest ? 32 + operand_position(a.bits1, c - 32) : operand_position(a.bits0, c);
+              *reinterpret_cast<uint16_t*>(qrow + (k >> 3) * 128 + (k & 7) * 2) =
+                  static_cast<uint16_t>((k4 < 2 ? h01 : h23) >> (16 * (k4 & 1)));
+            }
+          }
+          if (prod) {   // columns c, c + 64 side by side: lane l < 16 pairs up with lane l + 16
+            const uint32_t o01 = __shfl_xor_sync(kFull, h01, 16), o23 = __shfl_xor_sync(kFull, h23, 16);
+            if (lane < 16)
+              *reinterpret_cast<uint4*>(prow + 128 * lane) = make_uint4(prmt(h01, o01, 0x5410), prmt(h01, o01, 0x7632),
+                                                                        prmt(h23, o23, 0x5410), prmt(h23, o23, 0x7632));
           }
         }
       }
@@ -750,9 +783,9 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       warp_arrive(&ms.q_full, lane);
     }
 
-    float sum[NS];
+    uint64_t sum[NS / 2];   // packed pairs of fp32 sums
 #pragma unroll
-    for (int i = 0; i < NS; ++i) sum[i] = 0.f;
+    for (int i = 0; i < NS / 2; ++i) sum[i] = 0;
     const int r_first = kByRows ? s * NS : 0;          // this stream's rows of the tile
     const int* limit = ms.limit + r_first;
     float* ref = ms.ref[s];
@@ -777,13 +810,12 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
         for (int c = 0; c < NS; c += 16) tmem_ld16(tS + c, *reinterpret_cast<uint32_t(*)[16]>(y + c));
 #pragma unroll
         for (int c = 0; c < NS; c += 16) tmem_ld_wait_tied16(*reinterpret_cast<uint32_t(*)[16]>(y + c));
+        const uint64_t sc2 = pk2(sc, sc);
 #pragma unroll
-        for (int c = 0; c < NS; c += 4) {
-          const float4 m4 = rel ? *reinterpret_cast<const float4*>(ref + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-          x[c] = fmaf(x[c], sc, -m4.x);
-          x[c + 1] = fmaf(x[c + 1], sc, -m4.y);
-          x[c + 2] = fmaf(x[c + 2], sc, -m4.z);
-          x[c + 3] = fmaf(x[c + 3], sc, -m4.w);
+        for (int c = 0; c < NS; c += 4) {   // ref holds the negated references
+          const ulonglong2 m4 = rel ? *reinterpret_cast<const ulonglong2*>(ref + c) : make_ulonglong2(0, 0);
+          const float2 lo = up2(fma2(pk2(x[c], x[c + 1]), sc2, m4.x)), hi = up2(fma2(pk2(x[c + 2], x[c + 3]), sc2, m4.y));
+          x[c] = lo.x; x[c + 1] = lo.y; x[c + 2] = hi.x; x[c + 3] = hi.y;
         }
         if (masked) {
 #pragma unroll
@@ -799,7 +831,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       logits(true);
       float mx = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NS; ++c) mx = fmaxf(mx, x[c]);
+      for (int c = 0; c < NS; c += 2) mx = max3(mx, x[c], x[c + 1]);
       bool waited = i == 0;
       if (named_any(1 + s, mx > kTau)) {
         // raise the references to the tile's maxima
@@ -816,14 +848,14 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
         }
         named_sync(1 + s, 128);
         if (tok < NS) {
-          const float old = ref[tok];
+          const float old = -ref[tok];
           const float m = fmaxf(fmaxf(old, fmaxf(wmax[tok], wmax[NS + tok])), fmaxf(wmax[2 * NS + tok], wmax[3 * NS + tok]));
           fac[tok] = old == m ? 1.f : ex2(old - m);
-          ref[tok] = m;
+          ref[tok] = -m;
         }
         named_sync(1 + s, 128);
 #pragma unroll
-        for (int c = 0; c < NS; ++c) sum[c] *= fac[c];
+        for (int c = 0; c < NS; c += 2) sum[c / 2] = mul2(sum[c / 2], *reinterpret_cast<const uint64_t*>(fac + c));
         if (i > 0) {
 #pragma unroll 1
           for (int c = 0; c < used; c += 16) {
@@ -842,9 +874,10 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       for (int c = 0; c < NS; c += 16) {
         uint32_t p[8];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
+        for (int q = 0; q < 16; q += 2) {
           x[c + q] = ex2(x[c + q]);
-          sum[c + q] += x[c + q];
+          x[c + q + 1] = ex2(x[c + q + 1]);
+          sum[(c + q) / 2] = add2(sum[(c + q) / 2], pk2(x[c + q], x[c + q + 1]));
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) p[q] = h2bits(__floats2half2_rn(x[c + 2 * q], x[c + 2 * q + 1]));
@@ -864,7 +897,11 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     for (int c = 0; c < NS; c += 16) {
       float y[16];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) y[q] = sum[c + q];
+      for (int q = 0; q < 16; q += 2) {
+        const float2 v = up2(sum[(c + q) / 2]);
+        y[q] = v.x;
+        y[q + 1] = v.y;
+      }
       const float t = reduce16(y, lane, [](float p, float q) { return p + q; });
       if ((lane & 1) == 0) wsum[(warp & 3) * NS + c + (lane >> 1)] = t;
     }
@@ -878,10 +915,10 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       const float l0 = (w0[0] + w0[NS]) + (w0[2 * NS] + w0[3 * NS]);
       const float l1 = (w1[0] + w1[NS]) + (w1[2 * NS] + w1[3 * NS]);
       if (kByRows) {
-        jm[r_first + tok] = ref[tok];
+        jm[r_first + tok] = -ref[tok];
         jl[r_first + tok] = s ? l1 : l0;
       } else if (s == 0) {
-        const float m0 = ms.ref[0][tok], m1 = ms.ref[1][tok], m = fmaxf(m0, m1);
+        const float m0 = -ms.ref[0][tok], m1 = -ms.ref[1][tok], m = fmaxf(m0, m1);
         const float f0 = m0 == m ? 1.f : ex2(m0 - m), f1 = m1 == m ? 1.f : ex2(m1 - m);
         fac0[tok] = f0;
         fac1[tok] = f1;
