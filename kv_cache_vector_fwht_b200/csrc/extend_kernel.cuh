@@ -180,26 +180,34 @@ __device__ __forceinline__ int operand_position(int bits, int c) {
 }
 
 // Unpack the index words of 32 U channels to 16 U operand pairs in tensor memory; SCALED: times g.
-// All words are loaded first: the unpacking then runs without waiting for shared memory.
+// 32 channels at a time, the next words loaded ahead: the loop is kept rolled, because five roles
+// share an SM sub-partition's instruction fetch.
 template <int BITS, int U, bool SCALED>
 __device__ __forceinline__ void key_units(const uint8_t* row, const Levels& lv, __half2 g, uint32_t tcol) {
   constexpr int NP = level_pairs(BITS), WU = 16 / NP;   // pairs of a word, words of 32 channels
-  uint32_t w[U * WU];
-  if constexpr (!SCALED && U * WU % 4 == 0) {   // rows of 16, 32 or 64 bytes; grouped rows are aligned to words
+  uint32_t w[WU], n[WU];
+  auto load = [&](int u) {
+    const uint8_t* p = row + 4 * WU * u;
+    if constexpr (!SCALED && WU == 4) {   // rows of 16, 32 or 64 bytes; grouped rows are aligned to words
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      n[0] = x.x; n[1] = x.y; n[2] = x.z; n[3] = x.w;
+    } else if constexpr (!SCALED && WU == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      n[0] = x.x; n[1] = x.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < U * WU / 4; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * i);
-      w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+      for (int i = 0; i < WU; ++i) n[i] = reinterpret_cast<const uint32_t*>(p)[i];
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < U * WU; ++i) w[i] = reinterpret_cast<const uint32_t*>(row)[i];
-  }
-#pragma unroll
+  };
+  load(0);
+#pragma unroll 1
   for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int i = 0; i < WU; ++i) w[i] = n[i];
+    if (u + 1 < U) load(u + 1);
     uint32_t r[16];
 #pragma unroll
-    for (int i = 0; i < WU; ++i) unpack_levels<BITS>(w[WU * u + i], lv, *reinterpret_cast<uint32_t(*)[NP]>(r + NP * i));
+    for (int i = 0; i < WU; ++i) unpack_levels<BITS>(w[i], lv, *reinterpret_cast<uint32_t(*)[NP]>(r + NP * i));
     if constexpr (SCALED) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) r[i] = h2bits(__hmul2(bits_h2(r[i]), g));
@@ -464,12 +472,13 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
           const uint32_t rho = h2bits(__float2half2_rn(n16 > 0.f ? half_hi(nn) / n16 * a.sketch_ratio : 0.f));
           factor = n16 * a.key_scale0;
           const uint4 sg = *reinterpret_cast<const uint4*>(raw + o_sgn + 16 * tok);
-          const uint32_t inv[4] = {~sg.x, ~sg.y, ~sg.z, ~sg.w};
-#pragma unroll
+          uint32_t inv[4] = {~sg.x, ~sg.y, ~sg.z, ~sg.w};
+#pragma unroll 1
           for (int u = 0; u < 4; ++u) {
             uint32_t r[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = sign_level(inv[u], i, rho);
+            for (int i = 0; i < 16; ++i) r[i] = sign_level(inv[0], i, rho);
+            inv[0] = inv[1]; inv[1] = inv[2]; inv[2] = inv[3];
             tmem_st16(tk + 64 + 16 * u, r);
           }
         } else {
@@ -506,7 +515,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       // the lanes take the four groups in different orders, so that eight rows 64 (or 32) bytes
       // apart are read from different banks
       const int turn = a.vbits == 4 ? lane >> 1 : lane >> 2;
-#pragma unroll 2
+#pragma unroll 1
       for (int g0 = 0; g0 < 4; ++g0) {
         const int g = (g0 + turn) & 3;
         uint32_t p = there ? par[g] : 0u;
