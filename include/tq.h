@@ -311,7 +311,7 @@ typedef struct {
  *                 images and video: time, height, width)
  *   inv_freq_dev  fp32 rot_dim / 2
  *   axis_of_freq  host, rot_dim / 2 values in [0, n_axes); NULL = axis 0
- *   rot_dim       0 .. d, a multiple of 8; channels from rot_dim on are not turned
+ *   rot_dim       0 .. d, a multiple of 16; channels from rot_dim on are not turned
  *   interleaved   0: pair i is channels (i, i + rot_dim / 2); 1: channels (2i, 2i + 1) */
 typedef struct {
   const int32_t* pos_dev;

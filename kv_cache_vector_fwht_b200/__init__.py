@@ -124,8 +124,11 @@ class Heads(ctypes.Structure):
 
 class Rope(ctypes.Structure):
     _fields_ = [("pos_dev", c_void_p), ("inv_freq_dev", c_void_p),
-                ("axis_of_freq", c_void_p), ("n_axes", c_int32), ("rot_dim", c_int32),
+                ("axis_of_freq", ctypes.c_char_p), ("n_axes", c_int32), ("rot_dim", c_int32),
                 ("interleaved", c_int32)]
+
+
+_NO_HEADS = Heads(None, 0, 0, 0)
 
 
 _lib.tq_norm_rope.argtypes = [POINTER(Rope), c_int, c_int, c_int, c_int, c_int, Heads, Heads,
@@ -485,9 +488,8 @@ def _on_current_device(where: str, *tensors) -> None:
     import torch
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None:
-            _require(t.is_cuda and t.device.index == cur,
-                     f"{where}: tensors must be on the current CUDA device ({cur}), got {t.device}")
+        if t.get_device() != cur:   # -1: not on a GPU
+            raise ValueError(f"{where}: tensors must be on the current CUDA device ({cur}), got {t.device}")
 
 
 def _heads(x) -> Heads:
@@ -516,42 +518,46 @@ def tq_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weigh
     sequence; None: axis 0). q_weight / k_weight: 128 norm weights each, in the tensors' type. norm:
     whether to normalise; None: if a weight is given."""
     x = q if q is not None else k
-    _require(x is not None, "tq_norm_rope: q or k is needed")
-    batch, n_tokens = x.shape[0], x.shape[2]
-    none = Heads(None, 0, 0, 0)
+    _require(x is not None and x.dim() == 4, "tq_norm_rope: q or k is needed, (batch, heads, n_tokens, 128)")
+    batch, _, n_tokens, _ = x.shape
+    dtype, dev = x.dtype, x.device
     args = []
     for a, o, w in ((q, q_out, q_weight), (k, k_out, k_weight)):
         if a is None:
             _require(o is None, "tq_norm_rope: an output without its input")
-            args.append((0, none, none, None))
+            args += (0, _NO_HEADS, _NO_HEADS, None)
             continue
-        _require(o is not None and o.shape == a.shape, "tq_norm_rope: an output has its input's shape")
-        _require(a.dim() == 4 and a.shape[3] == D and a.shape[0] == batch and a.shape[2] == n_tokens,
-                 "tq_norm_rope: tensors are (batch, heads, n_tokens, 128)")
-        _require(a.stride(3) == 1 and o.stride(3) == 1, "tq_norm_rope: channels must be adjacent")
-        _require(a.dtype == x.dtype and o.dtype == x.dtype, "tq_norm_rope: one type for all tensors")
-        _require(w is None or (w.dtype == x.dtype and w.shape == (D,) and w.is_contiguous()),
-                 "tq_norm_rope: weights are 128 contiguous values of the tensors' type")
-        args.append((a.shape[1], _heads(a), _heads(o), _ptr(w)))
-    _require(positions.dtype.is_signed and positions.element_size() == 4 and not positions.is_floating_point()
-             and positions.is_contiguous() and tuple(positions.shape[-2:]) == (batch, n_tokens)
-             and positions.dim() in (2, 3),
-             "tq_norm_rope: positions are int32 (n_axes, batch, n_tokens), contiguous")
-    _require(inv_freq.dim() == 1 and inv_freq.is_contiguous() and _dtype_code(inv_freq) == TQ_F32,
-             "tq_norm_rope: inv_freq is a contiguous fp32 vector")
-    _on_current_device("tq_norm_rope", q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq)
+        shape = a.shape
+        if not (o is not None and o.shape == shape and len(shape) == 4 and shape[0] == batch
+                and shape[2] == n_tokens and shape[3] == D):
+            raise ValueError("tq_norm_rope: tensors are (batch, heads, n_tokens, 128), outputs as their inputs")
+        if not (a.dtype == dtype and o.dtype == dtype and a.device == dev and o.device == dev):
+            raise ValueError("tq_norm_rope: one type and one device for all tensors")
+        si, so = a.stride(), o.stride()
+        if si[3] != 1 or so[3] != 1:
+            raise ValueError("tq_norm_rope: channels must be adjacent")
+        if w is not None and not (w.dtype == dtype and w.shape == (D,) and w.is_contiguous() and w.device == dev):
+            raise ValueError("tq_norm_rope: weights are 128 contiguous values of the tensors' type")
+        args += (shape[1], Heads(a.data_ptr(), si[0], si[1], si[2]), Heads(o.data_ptr(), so[0], so[1], so[2]),
+                 _ptr(w))
+    pshape = positions.shape
+    if not (str(positions.dtype) == "torch.int32" and positions.is_contiguous() and len(pshape) in (2, 3)
+            and pshape[-2] == batch and pshape[-1] == n_tokens):
+        raise ValueError("tq_norm_rope: positions are int32 (n_axes, batch, n_tokens), contiguous")
+    if not (inv_freq.dim() == 1 and inv_freq.is_contiguous() and _dtype_code(inv_freq) == TQ_F32):
+        raise ValueError("tq_norm_rope: inv_freq is a contiguous fp32 vector")
+    _on_current_device("tq_norm_rope", x, positions, inv_freq)
     pairs = inv_freq.shape[0]
     axes = None
     if axis_of_freq is not None:
         _require(len(axis_of_freq) == pairs, "tq_norm_rope: one axis per frequency")
         axes = bytes(axis_of_freq)
-    rope = Rope(_ptr(positions), _ptr(inv_freq), ctypes.cast(axes, c_void_p) if axes else None,
-                positions.shape[0] if positions.dim() == 3 else 1, 2 * pairs, int(interleaved))
+    rope = Rope(positions.data_ptr(), inv_freq.data_ptr(), axes, pshape[0] if len(pshape) == 3 else 1,
+                2 * pairs, int(interleaved))
     if norm is None:
         norm = q_weight is not None or k_weight is not None
-    (nq, qi, qo, wq), (nk, ki, ko, wk) = args
-    _check(_lib.tq_norm_rope(ctypes.byref(rope), _dtype_code(x), batch, n_tokens, D, nq, qi, qo, wq,
-                             nk, ki, ko, wk, int(norm), eps, _stream(stream)), "tq_norm_rope")
+    _check(_lib.tq_norm_rope(ctypes.byref(rope), _dtype_code(x), batch, n_tokens, D, *args, int(norm), eps,
+                             _stream(stream)), "tq_norm_rope")
 
 
 def tq_extend_workspace_bytes(cache: KVCache, n_q_heads: int, n_tokens: int) -> int:

@@ -24,93 +24,123 @@ struct BoundsArgs {
   const DevTables* tab;
   int n_kv_heads, capacity, n_tokens, n_blocks;
   int row_words, n_norms;
-  int bits0, words0;     // the first channel group's code bits and index words (grouped: outliers)
-  int bits1;             // the second group's code bits (0: none)
+  int words0;            // index words of the first channel group (grouped: the outliers)
   float scale0, scale1;  // level scale / sqrt(channels of the group)
 };
 
+// The rows of a thread in flight, and its blocks: a block of threads walks up to kBlocks blocks of one
+// (sequence, KV head) with the next rows loaded before the present ones are used.
+constexpr int kInFlight = 4, kBlocks = 8;
+
+// Minima and maxima of one word's channels over kInFlight rows (their index words and score factors).
 template <int BITS>
-__device__ __forceinline__ void bounds_of_word(const BoundsArgs& a, const uint32_t* words, const uint16_t* norms,
-                                               int first, int step, int n, const Levels& lv, float scale, __half2* mn,
-                                               __half2* mx, int pair0) {
+__device__ __forceinline__ void bounds_step(const uint32_t (&w)[kInFlight], const float (&f)[kInFlight], const Levels& lv,
+                                            float* lo, float* hi) {
   constexpr int NP = level_pairs(BITS);
-  float lo[2 * NP], hi[2 * NP];
 #pragma unroll
-  for (int i = 0; i < 2 * NP; ++i) { lo[i] = INFINITY; hi[i] = -INFINITY; }
-  constexpr int U = 4;   // rows in flight
-  for (int r0 = first; r0 < n; r0 += U * step) {
-    uint32_t w[U];
-    uint16_t nr[U];
+  for (int u = 0; u < kInFlight; u += 2) {   // two rows a step: a three-way minimum takes both
+    uint32_t y0[NP], y1[NP];
+    unpack_levels<BITS>(w[u], lv, y0);
+    unpack_levels<BITS>(w[u + 1], lv, y1);
+    const uint64_t f0 = pk2(f[u], f[u]), f1 = pk2(f[u + 1], f[u + 1]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = min(r0 + u * step, n - 1);   // a row seen twice changes no minimum
-      w[u] = __ldg(words + static_cast<int64_t>(r) * a.row_words);
-      nr[u] = __ldg(norms + r * a.n_norms);
+    for (int i = 0; i < NP; ++i) {
+      const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(&y0[i])), l1 = __half22float2(*reinterpret_cast<const __half2*>(&y1[i]));
+      const float2 a0 = up2(mul2(pk2(l0.x, l0.y), f0)), a1 = up2(mul2(pk2(l1.x, l1.y), f1));
+      lo[2 * i] = min3(lo[2 * i], a0.x, a1.x);
+      hi[2 * i] = max3(hi[2 * i], a0.x, a1.x);
+      lo[2 * i + 1] = min3(lo[2 * i + 1], a0.y, a1.y);
+      hi[2 * i + 1] = max3(hi[2 * i + 1], a0.y, a1.y);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t y[NP];
-      unpack_levels<BITS>(w[u], lv, y);
-      const float f = __half2float(__ushort_as_half(nr[u])) * scale;
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float v0 = half_lo(y[i]) * f, v1 = half_hi(y[i]) * f;
-        lo[2 * i] = fminf(lo[2 * i], v0);
-        hi[2 * i] = fmaxf(hi[2 * i], v0);
-        lo[2 * i + 1] = fminf(lo[2 * i + 1], v1);
-        hi[2 * i + 1] = fmaxf(hi[2 * i + 1], v1);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {   // rounding is monotone: the minimum of the rounded is the rounded minimum
-    mn[pair0 + i] = __floats2half2_rn(lo[2 * i], lo[2 * i + 1]);
-    mx[pair0 + i] = __floats2half2_rn(hi[2 * i], hi[2 * i + 1]);
   }
 }
 
-__global__ void __launch_bounds__(kBT) k_block_bounds(const __grid_constant__ BoundsArgs a) {
+// B0, B1: code bits of the two channel groups (B1 = 0: one group).
+template <int B0, int B1>
+__global__ void __launch_bounds__(kBT, B0 == 1 || B1 == 1 ? 4 : 6) k_block_bounds(const __grid_constant__ BoundsArgs a) {
   __shared__ __half2 mn[kBT / 4][kD / 2], mx[kBT / 4][kD / 2];
   __shared__ __half res[2][kD];
   const int b = blockIdx.z, kv = blockIdx.y;
   const int len = min(a.len[b], a.capacity);
-  const int blk = max(0, len - a.n_tokens) / TQ_BLOCK + blockIdx.x;
-  const int n = min(TQ_BLOCK, len - blk * TQ_BLOCK);
-  if (n <= 0) return;
-  const int64_t row0 = (static_cast<int64_t>(b) * a.n_kv_heads + kv) * a.capacity + static_cast<int64_t>(blk) * TQ_BLOCK;
+  const int blk0 = max(0, len - a.n_tokens) / TQ_BLOCK + blockIdx.x * kBlocks;
+  const int n_rows = len - blk0 * TQ_BLOCK;
+  if (n_rows <= 0) return;
+  const int blocks = min(kBlocks, (n_rows + TQ_BLOCK - 1) / TQ_BLOCK);
+  const int64_t pair = static_cast<int64_t>(b) * a.n_kv_heads + kv;
+  const int64_t row0 = pair * a.capacity + static_cast<int64_t>(blk0) * TQ_BLOCK;
   const int groups = kBT / a.row_words;
   const int word = threadIdx.x % a.row_words, g = threadIdx.x / a.row_words;
-  const int used = min(groups, n);   // threads of a word that have a token
-  if (g < used) {
-    const bool second = a.bits1 != 0 && word >= a.words0;
-    const int bits = second ? a.bits1 : a.bits0;
-    const Levels lv = load_levels(a.tab, second);
-    const float scale = second ? a.scale1 : a.scale0;
-    const uint32_t* words = reinterpret_cast<const uint32_t*>(a.idx) + row0 * a.row_words + word;
-    const uint16_t* norms = a.norms + row0 * a.n_norms + second;
-    const int pair0 = second ? level_pairs(a.bits0) * a.words0 + (word - a.words0) * level_pairs(bits) : word * level_pairs(bits);
-    switch (bits) {
-      case 1: bounds_of_word<1>(a, words, norms, g, used, n, lv, scale, mn[g], mx[g], pair0); break;
-      case 2: bounds_of_word<2>(a, words, norms, g, used, n, lv, scale, mn[g], mx[g], pair0); break;
-      case 3: bounds_of_word<3>(a, words, norms, g, used, n, lv, scale, mn[g], mx[g], pair0); break;
-      default: bounds_of_word<4>(a, words, norms, g, used, n, lv, scale, mn[g], mx[g], pair0); break;
+  __half2* out = reinterpret_cast<__half2*>(a.bounds + (pair * a.n_blocks + blk0) * 2 * kD);
+  const bool second = B1 != 0 && word >= a.words0;
+  const Levels lv = load_levels(a.tab, second);
+  const float scale = second ? a.scale1 : a.scale0;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(a.idx) + row0 * a.row_words + word;
+  const uint16_t* norms = a.norms + row0 * a.n_norms + second;
+  const int steps = (TQ_BLOCK + kInFlight * groups - 1) / (kInFlight * groups);   // of a block
+  uint32_t w[kInFlight];
+  uint16_t nr[kInFlight];
+  auto load = [&](int it) {
+    const int blk = it / steps, first = blk * TQ_BLOCK, last = min(n_rows, first + TQ_BLOCK) - 1;
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      // a row seen twice changes no minimum (nor do the few threads beyond groups x words)
+      const int r = min(first + g + groups * (kInFlight * (it - blk * steps) + u), last);
+      w[u] = __ldg(words + static_cast<int64_t>(r) * a.row_words);
+      nr[u] = __ldg(norms + static_cast<int64_t>(r) * a.n_norms);
     }
+  };
+  constexpr int NP0 = level_pairs(B0), NP1 = B1 ? level_pairs(B1) : 1, NP = NP0 > NP1 ? NP0 : NP1;
+  float lo[2 * NP], hi[2 * NP];
+  load(0);
+#pragma unroll 1
+  for (int blk = 0; blk < blocks; ++blk) {
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) { lo[i] = INFINITY; hi[i] = -INFINITY; }
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s) {
+      uint32_t wc[kInFlight];
+      float f[kInFlight];
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        wc[u] = w[u];
+        f[u] = __half2float(__ushort_as_half(nr[u])) * scale;
+      }
+      if (blk * steps + s + 1 < blocks * steps) load(blk * steps + s + 1);
+      if (!second) bounds_step<B0>(wc, f, lv, lo, hi);
+      else if constexpr (B1 != 0) bounds_step<B1>(wc, f, lv, lo, hi);
+    }
+    if (g < groups) {   // rounding is monotone: the minimum of the rounded is the rounded minimum
+      const int p = second ? NP0 * a.words0 + (word - a.words0) * NP1 : word * NP0, n = second ? NP1 : NP0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (i < n) {
+          mn[g][p + i] = __floats2half2_rn(lo[2 * i], lo[2 * i + 1]);
+          mx[g][p + i] = __floats2half2_rn(hi[2 * i], hi[2 * i + 1]);
+        }
+      }
+    }
+    __syncthreads();
+    {
+      const int p = threadIdx.x & 63, which = threadIdx.x >> 6;
+      __half2 v;
+      if (which) {
+        v = mx[0][p];
+#pragma unroll 8
+        for (int i = 1; i < groups; ++i) v = __hmax2(v, mx[i][p]);
+      } else {
+        v = mn[0][p];
+#pragma unroll 8
+        for (int i = 1; i < groups; ++i) v = __hmin2(v, mn[i][p]);
+      }
+      const int pairs0 = NP0 * a.words0;
+      const bool rest = p >= pairs0;
+      const int bits = rest ? B1 : B0, q = rest ? p - pairs0 : p, c0 = rest ? 2 * pairs0 : 0;
+      res[which][c0 + level_channel(bits, q, 0)] = __low2half(v);
+      res[which][c0 + level_channel(bits, q, 1)] = __high2half(v);
+    }
+    __syncthreads();
+    out[blk * kD + threadIdx.x] = reinterpret_cast<const __half2*>(&res[0][0])[threadIdx.x];
   }
-  __syncthreads();
-  if (threadIdx.x < kD) {
-    const int p = threadIdx.x & 63, which = threadIdx.x >> 6;
-    __half2 v = which ? mx[0][p] : mn[0][p];
-    for (int i = 1; i < used; ++i) v = which ? __hmax2(v, mx[i][p]) : __hmin2(v, mn[i][p]);
-    const int pairs0 = level_pairs(a.bits0) * a.words0;
-    const bool second = p >= pairs0;
-    const int bits = second ? a.bits1 : a.bits0, q = second ? p - pairs0 : p, c0 = second ? 2 * pairs0 : 0;
-    res[which][c0 + level_channel(bits, q, 0)] = __low2half(v);
-    res[which][c0 + level_channel(bits, q, 1)] = __high2half(v);
-  }
-  __syncthreads();
-  __half2* out = reinterpret_cast<__half2*>(
-      a.bounds + ((static_cast<int64_t>(b) * a.n_kv_heads + kv) * a.n_blocks + blk) * 2 * kD);
-  out[threadIdx.x] = reinterpret_cast<const __half2*>(&res[0][0])[threadIdx.x];
 }
 
 // ------------------------------------------------------------------------------- selection
@@ -380,21 +410,27 @@ tq_status launch_block_bounds(const tq_quantizer* q, const tq_kv_cache* c, void*
   a.row_words = q->layout.idx_bytes / 4;
   a.n_norms = q->layout.n_norms;
   if (q->mode == TQ_MODE_GROUPED) {
-    a.bits0 = q->bits + 1;
-    a.bits1 = q->bits;
-    a.words0 = storage_width_c(a.bits0);
+    a.words0 = storage_width_c(q->bits + 1);
     a.scale0 = q->lv_scale[0] / std::sqrt(32.f);
     a.scale1 = q->lv_scale[1] / std::sqrt(96.f);
   } else {
-    a.bits0 = q->mode == TQ_MODE_PROD ? q->bits - 1 : q->bits;
-    a.bits1 = 0;
     a.words0 = a.row_words;
     a.scale0 = a.scale1 = q->lv_scale[0] / std::sqrt(static_cast<float>(kD));
   }
   // the blocks that n_tokens tokens can touch, wherever they begin
   const int64_t span = (static_cast<int64_t>(n_tokens) + TQ_BLOCK - 2) / TQ_BLOCK + 1;
-  const dim3 grid(static_cast<unsigned>(span < a.n_blocks ? span : a.n_blocks), c->n_kv_heads, c->batch);
-  k_block_bounds<<<grid, kBT, 0, st>>>(a);
+  const int64_t most = span < a.n_blocks ? span : a.n_blocks;
+  const dim3 grid(static_cast<unsigned>((most + kBlocks - 1) / kBlocks), c->n_kv_heads, c->batch);
+  const int bits = q->mode == TQ_MODE_PROD ? q->bits - 1 : q->bits;
+  switch (q->mode == TQ_MODE_GROUPED ? 4 + bits : bits) {
+    case 1: k_block_bounds<1, 0><<<grid, kBT, 0, st>>>(a); break;
+    case 2: k_block_bounds<2, 0><<<grid, kBT, 0, st>>>(a); break;
+    case 3: k_block_bounds<3, 0><<<grid, kBT, 0, st>>>(a); break;
+    case 4: k_block_bounds<4, 0><<<grid, kBT, 0, st>>>(a); break;
+    case 5: k_block_bounds<2, 1><<<grid, kBT, 0, st>>>(a); break;
+    case 6: k_block_bounds<3, 2><<<grid, kBT, 0, st>>>(a); break;
+    default: k_block_bounds<4, 3><<<grid, kBT, 0, st>>>(a); break;
+  }
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
 }
 

@@ -570,7 +570,7 @@ tq_status tq_norm_rope(const tq_rope* rope, int dtype, int batch, int n_tokens, 
                        const void* k_weight, int norm, float eps, void* stream) {
   if (!rope || batch < 0 || n_tokens < 0 || n_q_heads < 0 || n_k_heads < 0) return TQ_EINVAL;
   if (d != kD || !known_dtype(dtype)) return TQ_EUNSUPPORTED;
-  if (rope->rot_dim < 0 || rope->rot_dim > kD || rope->rot_dim % 8) return TQ_EINVAL;
+  if (rope->rot_dim < 0 || rope->rot_dim > kD || rope->rot_dim % 16) return TQ_EINVAL;
   if (norm && !(eps >= 0.f)) return TQ_EINVAL;
   if (rope->rot_dim > 0) {
     if (!rope->pos_dev || !rope->inv_freq_dev || rope->n_axes < 1 || rope->n_axes > 255) return TQ_EINVAL;
