@@ -1,5 +1,6 @@
 // Block bounds of the packed keys and the choice of blocks for a sparse decode step
 // (tq_block_bounds, tq_select_blocks).
+#include <algorithm>
 #include <cmath>
 
 #include "packed.cuh"
@@ -8,12 +9,17 @@ namespace tq {
 namespace {
 
 // ------------------------------------------------------------------------------- bounds
-// min and max over a block's tokens of n16 c[idx_j] / sqrt(d), channel by channel. One block of
-// threads per token block; thread = (word of the row, every G-th token): it unpacks its index
-// words to fp16 levels, scales them by the token's norm and keeps the channels' minimum and maximum
-// in registers (fp32), then the G threads of a word are joined through shared memory in fp16, the
-// type of the result: one rounding of the product.
-// Reads of a row are contiguous over the threads; the work is bound by HBM for long ranges.
+// min and max over a block's tokens of n16 c[idx_j] / sqrt(d), channel by channel. A block of threads
+// walks a few token blocks of one (sequence, KV head); thread = (word of the row, every G-th token):
+// it unpacks its index words to fp16 levels, scales them by the token's norm in fp32 and keeps the
+// channels' minimum and maximum in registers, the next block's rows being loaded meanwhile. Then the
+// threads that share a word are joined in fp16, the type of the result (rounding is monotone, so
+// the minimum of the rounded is the rounded minimum): by exchanges within the warp, where the row's
+// words divide it, and in shared memory.
+// Bound by instructions: a value costs a conversion, a product and a share of two three-way minima
+// beside its lookup, against half a byte read: 35 us for 8 x 4 x 20000 rows of 2-bit codes (36 bytes
+// a row read, 31 MB), where HBM alone would take 5. Packed fp16 products are no faster to speak of (34
+// us) and half as far again from the exact bounds.
 constexpr int kBT = 128;
 
 struct BoundsArgs {
@@ -22,23 +28,16 @@ struct BoundsArgs {
   const int32_t* len;
   __half* bounds;
   const DevTables* tab;
-  int n_kv_heads, capacity, n_tokens, n_blocks;
-  int row_words, n_norms;
-  int words0;            // index words of the first channel group (grouped: the outliers)
+  int n_kv_heads, capacity, n_tokens, n_blocks, per_cta, n_norms;
   float scale0, scale1;  // level scale / sqrt(channels of the group)
 };
 
-// The rows of a thread in flight, and its blocks: a block of threads walks up to kBlocks blocks of one
-// (sequence, KV head) with the next rows loaded before the present ones are used.
-constexpr int kInFlight = 4, kBlocks = 8;
-
-// Minima and maxima of one word's channels over kInFlight rows (their index words and score factors).
-template <int BITS>
-__device__ __forceinline__ void bounds_step(const uint32_t (&w)[kInFlight], const float (&f)[kInFlight], const Levels& lv,
-                                            float* lo, float* hi) {
+// Minima lo and maxima hi of one word's channels over R rows (their index words and score factors).
+template <int BITS, int R>
+__device__ __forceinline__ void bounds_step(const uint32_t (&w)[R], const float (&f)[R], const Levels& lv, float* lo, float* hi) {
   constexpr int NP = level_pairs(BITS);
 #pragma unroll
-  for (int u = 0; u < kInFlight; u += 2) {   // two rows a step: a three-way minimum takes both
+  for (int u = 0; u < R; u += 2) {   // two rows a step: a three-way minimum takes both
     uint32_t y0[NP], y1[NP];
     unpack_levels<BITS>(w[u], lv, y0);
     unpack_levels<BITS>(w[u + 1], lv, y1);
@@ -55,91 +54,116 @@ __device__ __forceinline__ void bounds_step(const uint32_t (&w)[kInFlight], cons
   }
 }
 
+// Exchange with the lane M away: of N results a lane keeps the half that its bit M names.
+template <int M, int N>
+__device__ __forceinline__ void join_lanes(__half2* v, int lane) {
+  const bool up = lane & M;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const __half2 mine = up ? v[i + N / 2] : v[i], theirs = up ? v[i] : v[i + N / 2];
+    v[i] = __hmin2(mine, __shfl_xor_sync(kFull, theirs, M));
+  }
+}
+
 // B0, B1: code bits of the two channel groups (B1 = 0: one group).
 template <int B0, int B1>
 __global__ void __launch_bounds__(kBT, B0 == 1 || B1 == 1 ? 4 : 6) k_block_bounds(const __grid_constant__ BoundsArgs a) {
-  __shared__ __half2 mn[kBT / 4][kD / 2], mx[kBT / 4][kD / 2];
+  constexpr bool kGrouped = B1 != 0;
+  constexpr int kWords0 = (kGrouped ? 1 : 4) * storage_width_c(B0);               // 32-bit words of the first group
+  constexpr int kWords = kWords0 + (kGrouped ? 3 * storage_width_c(kGrouped ? B1 : 1) : 0);
+  constexpr int kGroups = kBT / kWords;      // threads that share a word
+  constexpr int kR = kWords <= 5 ? 2 : 4;    // rows in flight
+  constexpr int kSteps = (TQ_BLOCK + kR * kGroups - 1) / (kR * kGroups);
+  constexpr int NP0 = level_pairs(B0), NP1 = kGrouped ? level_pairs(kGrouped ? B1 : 1) : 1, NP = NP0 > NP1 ? NP0 : NP1;
+  constexpr int kParts = kGrouped ? kGroups : kBT / 32;
+  __shared__ __align__(16) __half2 part[kParts][2][kD / 2];   // minima and negated maxima to be joined
   __shared__ __half res[2][kD];
-  const int b = blockIdx.z, kv = blockIdx.y;
+  const int b = blockIdx.z, kv = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int len = min(a.len[b], a.capacity);
-  const int blk0 = max(0, len - a.n_tokens) / TQ_BLOCK + blockIdx.x * kBlocks;
+  const int blk0 = max(0, len - a.n_tokens) / TQ_BLOCK + blockIdx.x * a.per_cta;
   const int n_rows = len - blk0 * TQ_BLOCK;
   if (n_rows <= 0) return;
-  const int blocks = min(kBlocks, (n_rows + TQ_BLOCK - 1) / TQ_BLOCK);
+  const int blocks = min(a.per_cta, (n_rows + TQ_BLOCK - 1) / TQ_BLOCK);
   const int64_t pair = static_cast<int64_t>(b) * a.n_kv_heads + kv;
   const int64_t row0 = pair * a.capacity + static_cast<int64_t>(blk0) * TQ_BLOCK;
-  const int groups = kBT / a.row_words;
-  const int word = threadIdx.x % a.row_words, g = threadIdx.x / a.row_words;
+  const int word = tid % kWords, g = tid / kWords;
   __half2* out = reinterpret_cast<__half2*>(a.bounds + (pair * a.n_blocks + blk0) * 2 * kD);
-  const bool second = B1 != 0 && word >= a.words0;
+  const bool second = kGrouped && word >= kWords0;
   const Levels lv = load_levels(a.tab, second);
   const float scale = second ? a.scale1 : a.scale0;
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(a.idx) + row0 * a.row_words + word;
-  const uint16_t* norms = a.norms + row0 * a.n_norms + second;
-  const int steps = (TQ_BLOCK + kInFlight * groups - 1) / (kInFlight * groups);   // of a block
-  uint32_t w[kInFlight];
-  uint16_t nr[kInFlight];
+  const int n_norms = kGrouped ? 2 : a.n_norms;   // prod rows hold ||r|| too
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(a.idx) + row0 * kWords + word;
+  const uint16_t* norms = a.norms + row0 * n_norms + second;
+  uint32_t w[kR];
+  uint16_t nr[kR];
+  // rows of step `it`; a row seen twice changes no minimum (nor do the few threads beyond groups x words)
   auto load = [&](int it) {
-    const int blk = it / steps, first = blk * TQ_BLOCK, last = min(n_rows, first + TQ_BLOCK) - 1;
+    const int first = it / kSteps * TQ_BLOCK, last = min(n_rows, first + TQ_BLOCK) - 1;
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
-      // a row seen twice changes no minimum (nor do the few threads beyond groups x words)
-      const int r = min(first + g + groups * (kInFlight * (it - blk * steps) + u), last);
-      w[u] = __ldg(words + static_cast<int64_t>(r) * a.row_words);
-      nr[u] = __ldg(norms + static_cast<int64_t>(r) * a.n_norms);
+    for (int u = 0; u < kR; ++u) {
+      const int r = min(first + g + kGroups * (kR * (it % kSteps) + u), last);
+      w[u] = __ldg(words + r * kWords);
+      nr[u] = __ldg(norms + r * n_norms);
     }
   };
-  constexpr int NP0 = level_pairs(B0), NP1 = B1 ? level_pairs(B1) : 1, NP = NP0 > NP1 ? NP0 : NP1;
-  float lo[2 * NP], hi[2 * NP];
   load(0);
 #pragma unroll 1
   for (int blk = 0; blk < blocks; ++blk) {
+    float lo[2 * NP], hi[2 * NP];
 #pragma unroll
     for (int i = 0; i < 2 * NP; ++i) { lo[i] = INFINITY; hi[i] = -INFINITY; }
-#pragma unroll 1
-    for (int s = 0; s < steps; ++s) {
-      uint32_t wc[kInFlight];
-      float f[kInFlight];
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
+    for (int s = 0; s < kSteps; ++s) {
+      uint32_t wc[kR];
+      float f[kR];
+#pragma unroll
+      for (int u = 0; u < kR; ++u) {
         wc[u] = w[u];
         f[u] = __half2float(__ushort_as_half(nr[u])) * scale;
       }
-      if (blk * steps + s + 1 < blocks * steps) load(blk * steps + s + 1);
-      if (!second) bounds_step<B0>(wc, f, lv, lo, hi);
-      else if constexpr (B1 != 0) bounds_step<B1>(wc, f, lv, lo, hi);
+      if (blk * kSteps + s + 1 < blocks * kSteps) load(blk * kSteps + s + 1);
+      if (!second) bounds_step<B0, kR>(wc, f, lv, lo, hi);
+      else if constexpr (kGrouped) bounds_step<B1, kR>(wc, f, lv, lo, hi);
     }
-    if (g < groups) {   // rounding is monotone: the minimum of the rounded is the rounded minimum
-      const int p = second ? NP0 * a.words0 + (word - a.words0) * NP1 : word * NP0, n = second ? NP1 : NP0;
+    __half2 v[2 * NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      v[i] = __floats2half2_rn(lo[2 * i], lo[2 * i + 1]);
+      v[NP + i] = __floats2half2_rn(-hi[2 * i], -hi[2 * i + 1]);
+    }
+    if constexpr (!kGrouped) {
+      // 4, 8 or 16 words: the lanes of a warp that share a word end with 4 of its 2 NP results each
+      join_lanes<16, 2 * NP>(v, lane);
+      if constexpr (kWords <= 8) join_lanes<8, NP>(v, lane);
+      if constexpr (kWords <= 4) join_lanes<4, NP / 2>(v, lane);
+      const int at = word * NP + (kWords <= 8 ? (lane >> 3 & 1) * (NP / 2) : 0) + (kWords <= 4 ? (lane >> 2 & 1) * (NP / 4) : 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[tid >> 5][lane >> 4][at + i] = v[i];
+    } else if (g < kGroups) {
+      const int p = second ? NP0 * kWords0 + (word - kWords0) * NP1 : word * NP0, n = second ? NP1 : NP0;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         if (i < n) {
-          mn[g][p + i] = __floats2half2_rn(lo[2 * i], lo[2 * i + 1]);
-          mx[g][p + i] = __floats2half2_rn(hi[2 * i], hi[2 * i + 1]);
+          part[g][0][p + i] = v[i];
+          part[g][1][p + i] = v[NP + i];
         }
       }
     }
     __syncthreads();
     {
-      const int p = threadIdx.x & 63, which = threadIdx.x >> 6;
-      __half2 v;
-      if (which) {
-        v = mx[0][p];
-#pragma unroll 8
-        for (int i = 1; i < groups; ++i) v = __hmax2(v, mx[i][p]);
-      } else {
-        v = mn[0][p];
-#pragma unroll 8
-        for (int i = 1; i < groups; ++i) v = __hmin2(v, mn[i][p]);
-      }
-      const int pairs0 = NP0 * a.words0;
-      const bool rest = p >= pairs0;
-      const int bits = rest ? B1 : B0, q = rest ? p - pairs0 : p, c0 = rest ? 2 * pairs0 : 0;
-      res[which][c0 + level_channel(bits, q, 0)] = __low2half(v);
-      res[which][c0 + level_channel(bits, q, 1)] = __high2half(v);
+      const int p = tid & 63, which = tid >> 6;
+      __half2 x = part[0][which][p];
+#pragma unroll 4
+      for (int i = 1; i < kParts; ++i) x = __hmin2(x, part[i][which][p]);
+      if (which) x = __hneg2(x);
+      constexpr int pairs0 = NP0 * kWords0;
+      const bool rest = kGrouped && p >= pairs0;
+      const int q = rest ? p - pairs0 : p, c0 = rest ? 2 * pairs0 : 0;
+      res[which][c0 + (rest ? level_channel(kGrouped ? B1 : 4, q, 0) : level_channel(B0, q, 0))] = __low2half(x);
+      res[which][c0 + (rest ? level_channel(kGrouped ? B1 : 4, q, 1) : level_channel(B0, q, 1))] = __high2half(x);
     }
     __syncthreads();
-    out[blk * kD + threadIdx.x] = reinterpret_cast<const __half2*>(&res[0][0])[threadIdx.x];
+    out[blk * kD + tid] = reinterpret_cast<const __half2*>(&res[0][0])[tid];
   }
 }
 
@@ -407,20 +431,21 @@ tq_status launch_block_bounds(const tq_quantizer* q, const tq_kv_cache* c, void*
   a.capacity = c->capacity;
   a.n_tokens = n_tokens;
   a.n_blocks = block_count(c->capacity);
-  a.row_words = q->layout.idx_bytes / 4;
-  a.n_norms = q->layout.n_norms;
   if (q->mode == TQ_MODE_GROUPED) {
-    a.words0 = storage_width_c(q->bits + 1);
     a.scale0 = q->lv_scale[0] / std::sqrt(32.f);
     a.scale1 = q->lv_scale[1] / std::sqrt(96.f);
   } else {
-    a.words0 = a.row_words;
-    a.scale0 = a.scale1 = q->lv_scale[0] / std::sqrt(static_cast<float>(kD));
+    a.scale0 = q->lv_scale[0] / std::sqrt(static_cast<float>(kD));
+    a.scale1 = 0.f;
   }
+  a.n_norms = q->layout.n_norms;
   // the blocks that n_tokens tokens can touch, wherever they begin
   const int64_t span = (static_cast<int64_t>(n_tokens) + TQ_BLOCK - 2) / TQ_BLOCK + 1;
   const int64_t most = span < a.n_blocks ? span : a.n_blocks;
-  const dim3 grid(static_cast<unsigned>((most + kBlocks - 1) / kBlocks), c->n_kv_heads, c->batch);
+  // up to 8 blocks a block of threads, but several rounds over the SMs so that the last one is short
+  const int64_t all = most * c->n_kv_heads * c->batch;
+  a.per_cta = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, all / (8 * 6 * std::max(1, sm_count(q->device))))));
+  const dim3 grid(static_cast<unsigned>((most + a.per_cta - 1) / a.per_cta), c->n_kv_heads, c->batch);
   const int bits = q->mode == TQ_MODE_PROD ? q->bits - 1 : q->bits;
   switch (q->mode == TQ_MODE_GROUPED ? 4 + bits : bits) {
     case 1: k_block_bounds<1, 0><<<grid, kBT, 0, st>>>(a); break;
