@@ -182,6 +182,7 @@ constexpr int kHG = 4;       // heads scored at a time
 constexpr int kHS = 16;      // rotated heads held in shared memory
 constexpr int kBPW = 8;      // blocks a warp scores
 constexpr int kBins = 1024;
+constexpr int kNearKeys = kHS * kD;   // keys that fit the rotated heads' shared memory (2048 blocks: 131072 tokens)
 constexpr unsigned long long kAlways = ~0ull;
 
 struct SelectArgs {
@@ -240,7 +241,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums) {
 }
 
 // The blocks of one (sequence, KV head), by all threads of the block.
-__device__ void pick_blocks(const SelectArgs& a, int pair, int nb) {
+__device__ void pick_blocks(const SelectArgs& a, int pair, int nb, unsigned long long* near) {
   __shared__ unsigned hist[kBins];
   __shared__ int sums[kSW];
   __shared__ unsigned long long s_lo, s_hi;
@@ -251,14 +252,20 @@ __device__ void pick_blocks(const SelectArgs& a, int pair, int nb) {
     for (int i = tid; i < a.n_select; i += kST) ids[i] = i < nb ? i : -1;
     return;
   }
+  // the keys are read several times: from shared memory where they fit
   const unsigned long long* keys = a.keys + static_cast<int64_t>(pair) * a.n_blocks;
+  if (nb <= kNearKeys) {
+    for (int i = tid; i < nb; i += kST) near[i] = __ldcg(keys + i);
+    __syncthreads();
+    keys = near;
+  }
   int need = a.n_select - a.n_sink - a.n_recent;   // nb > n_select: the two ranges do not meet
   unsigned long long T = kAlways;                  // the smallest key chosen ...
   int ties = 0;                                    // ... and how many of its equals
   if (need > 0) {
     unsigned long long lo = ~0ull, hi = 0;
     for (int i = tid; i < nb; i += kST) {
-      const unsigned long long k = __ldcg(keys + i);
+      const unsigned long long k = keys[i];
       if (k != kAlways) { lo = min(lo, k); hi = max(hi, k); }
     }
     if (tid == 0) { s_lo = ~0ull; s_hi = 0; }
@@ -276,7 +283,7 @@ __device__ void pick_blocks(const SelectArgs& a, int pair, int nb) {
       for (int i = tid; i < kBins; i += kST) hist[i] = 0;
       __syncthreads();
       for (int i = tid; i < nb; i += kST) {
-        const unsigned long long k = __ldcg(keys + i);
+        const unsigned long long k = keys[i];
         if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> s], 1u);
       }
       __syncthreads();
@@ -312,7 +319,7 @@ __device__ void pick_blocks(const SelectArgs& a, int pair, int nb) {
   const int i0 = min(nb, tid * per), i1 = min(nb, i0 + per);
   int eq = 0, more = 0;
   for (int i = i0; i < i1; ++i) {
-    const unsigned long long k = __ldcg(keys + i);
+    const unsigned long long k = keys[i];
     eq += k == T && T != kAlways;
     more += k > T || k == kAlways;
   }
@@ -321,14 +328,14 @@ __device__ void pick_blocks(const SelectArgs& a, int pair, int nb) {
   const int end = block_scan(more + eq_taken, sums);
   int at = end - more - eq_taken, e = 0;
   for (int i = i0; i < i1; ++i) {
-    const unsigned long long k = __ldcg(keys + i);
+    const unsigned long long k = keys[i];
     bool take = k > T || k == kAlways;
     if (!take && k == T) take = e++ < eq_taken;
     if (take) ids[at++] = i;
   }
 }
 
-__global__ void __launch_bounds__(kST) k_select_blocks(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kST, 1) k_select_blocks(const __grid_constant__ SelectArgs a) {
   __shared__ double qs[kHS][kD];
   __shared__ bool last;
   const int b = blockIdx.z, kv = blockIdx.y, pair = b * a.n_kv_heads + kv;
@@ -337,10 +344,19 @@ __global__ void __launch_bounds__(kST) k_select_blocks(const __grid_constant__ S
   const int nb = (len + TQ_BLOCK - 1) / TQ_BLOCK;
   const int h0 = a.heads.start[kv], nh = a.heads.start[kv + 1] - h0;
   const int blk0 = (blockIdx.x * kSW + w) * kBPW;
-  if (nb > a.n_select) {   // else every block is chosen and no score is needed
-    double best[kBPW];
+  // the bounds are on their way while the heads are rotated; blocks past the last repeat it
+  uint2 lo2[kBPW], hi2[kBPW];
+  if (nb > a.n_select && static_cast<int>(blockIdx.x) * kSW * kBPW < nb) {
 #pragma unroll
-    for (int i = 0; i < kBPW; ++i) best[i] = nh ? -INFINITY : 0.0;
+    for (int i = 0; i < kBPW; ++i) {
+      const uint2* p = reinterpret_cast<const uint2*>(
+          a.bounds + (static_cast<int64_t>(pair) * a.n_blocks + min(blk0 + i, nb - 1)) * 2 * kD) + lane;
+      lo2[i] = __ldg(p);
+      hi2[i] = __ldg(p + 32);
+    }
+  }
+  if (nb > a.n_select) {   // else every block is chosen and no score is needed
+    double best = nh ? -INFINITY : 0.0;   // of block blk0 + lane / 4
     if (static_cast<int>(blockIdx.x) * kSW * kBPW < nb) {
       for (int r0 = 0; r0 < nh; r0 += kHS) {
         const int nr = min(kHS, nh - r0);
@@ -359,62 +375,60 @@ __global__ void __launch_bounds__(kST) k_select_blocks(const __grid_constant__ S
           for (int h = 0; h < kHG; ++h)
 #pragma unroll
             for (int i = 0; i < 4; ++i) q[h][i] = qs[g + h][4 * lane + i];
+          double s[kBPW * kHG];   // (block, head) partial sums of this lane's channels
 #pragma unroll
           for (int i = 0; i < kBPW; ++i) {
-            const int blk = blk0 + i;
-            if (blk >= nb) break;
-            const uint2* p = reinterpret_cast<const uint2*>(a.bounds + (static_cast<int64_t>(pair) * a.n_blocks + blk) * 2 * kD) + lane;
-            const uint2 lo2 = __ldg(p), hi2 = __ldg(p + 32);
-            const float lo[4] = {half_lo(lo2.x), half_hi(lo2.x), half_lo(lo2.y), half_hi(lo2.y)};
-            const float hi[4] = {half_lo(hi2.x), half_hi(hi2.x), half_lo(hi2.y), half_hi(hi2.y)};
-            double s[kHG] = {0.0, 0.0, 0.0, 0.0};
+            const float lo[4] = {half_lo(lo2[i].x), half_hi(lo2[i].x), half_lo(lo2[i].y), half_hi(lo2[i].y)};
+            const float hi[4] = {half_lo(hi2[i].x), half_hi(hi2[i].x), half_lo(hi2[i].y), half_hi(hi2[i].y)};
+#pragma unroll
+            for (int h = 0; h < kHG; ++h) s[i * kHG + h] = 0.0;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               // fp32 sums of two fp16 numbers would round: fp64 keeps them
               const double l = lo[c], u = hi[c], mid = l + u, rad = u - l;
 #pragma unroll
-              for (int h = 0; h < kHG; ++h) s[h] = fma(q[h][c], mid, fma(fabs(q[h][c]), rad, s[h]));
+              for (int h = 0; h < kHG; ++h) s[i * kHG + h] = fma(q[h][c], mid, fma(fabs(q[h][c]), rad, s[i * kHG + h]));
             }
-            // sums over the lanes: each exchange halves the heads a lane carries
-            const bool up = lane & 16, up2 = lane & 8;
-            double x0 = (up ? s[2] : s[0]) + shfl_xor_d(up ? s[0] : s[2], 16);
-            double x1 = (up ? s[3] : s[1]) + shfl_xor_d(up ? s[1] : s[3], 16);
-            double x = (up2 ? x1 : x0) + shfl_xor_d(up2 ? x0 : x1, 8);
-            x += shfl_xor_d(x, 4);
-            x += shfl_xor_d(x, 2);
-            x += shfl_xor_d(x, 1);
-            // the largest over the four heads; a NaN stays
-#pragma unroll
-            for (int m = 8; m <= 16; m <<= 1) {
-              const double o = shfl_xor_d(x, m);
-              x = isnan(o) || o > x ? o : x;
-            }
-            if (isnan(x) || x > best[i]) best[i] = x;
           }
+          // Sums over the lanes: each exchange halves the results a lane carries, 32 results end in
+          // 32 lanes (block lane / 4, head lane % 4) after 31 exchanges that overlap.
+          static_assert(kBPW * kHG == 32, "a result per lane");
+#pragma unroll
+          for (int m = 16, n = 16; m >= 1; m >>= 1, n >>= 1) {
+            const bool up = lane & m;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+              const double mine = up ? s[i + n] : s[i], theirs = up ? s[i] : s[i + n];
+              s[i] = mine + shfl_xor_d(theirs, m);
+            }
+          }
+          // the largest over the four heads; a NaN stays
+          double x = s[0];
+#pragma unroll
+          for (int m = 1; m <= 2; m <<= 1) {
+            const double o = shfl_xor_d(x, m);
+            x = isnan(o) || o > x ? o : x;
+          }
+          if (isnan(x) || x > best) best = x;
         }
       }
     }
-    if (lane == 0) {
-#pragma unroll
-      for (int i = 0; i < kBPW; ++i) {
-        const int blk = blk0 + i;
-        if (blk < nb)
-          a.keys[static_cast<int64_t>(pair) * a.n_blocks + blk] =
-              blk < a.n_sink || blk >= nb - a.n_recent ? kAlways : order_key(best[i]);
-      }
-    }
+    const int blk = blk0 + (lane >> 2);
+    if ((lane & 3) == 0 && blk < nb)
+      a.keys[static_cast<int64_t>(pair) * a.n_blocks + blk] =
+          blk < a.n_sink || blk >= nb - a.n_recent ? kAlways : order_key(best);
   }
   // the last block of threads of this (sequence, KV head) picks
-  __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
+    __threadfence();   // after the barrier: it stands for all threads' keys
     last = atomicAdd(a.counters + pair, 1) == static_cast<int>(gridDim.x) - 1;
     if (last) a.counters[pair] = 0;
   }
   __syncthreads();
   if (last) {
     __threadfence();
-    pick_blocks(a, pair, nb);
+    pick_blocks(a, pair, nb, reinterpret_cast<unsigned long long*>(&qs[0][0]));
   }
 }
 

@@ -968,9 +968,9 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     if (n_splits > 1) {
       // the last block of threads of this item joins the splits, in their order
       const int first = blockIdx.x - split;
-      __threadfence();
       named_sync(3, 256);
       if (tid == 32 * wS) {
+        __threadfence();   // after the barrier: it stands for all threads' records
         int* counter = a.counters + first;
         ms.last = atomicAdd(counter, 1) == n_splits - 1;
         if (ms.last) *counter = 0;
