@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
         tc_fence_after();
         // lane = sketch row j; a stream's warps take half of the query rows
         const int k = kD + operand_position(1, tok);
-        constexpr int kCols = N / 2 < 16 ? 16 : N / 2;   // N = 16: the first stream takes all of them
+        constexpr int kCols = (N / 2 + 15) / 16 * 16;   // whole chunks of 16; the second stream takes the rest
 #pragma unroll 1
         for (int c = s * kCols; c < min(N, (s + 1) * kCols); c += 16) {
           uint32_t x[16];
