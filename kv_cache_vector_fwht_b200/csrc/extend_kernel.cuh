@@ -319,8 +319,9 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
   const int nt = share + (split < more);
 
   // The softmax warps read the query rows for the largest norm while the others set up: warp w takes
-  // rows w, w + 8, ..., up to four at a time so that their loads overlap. Up to 32 rows stay in
-  // registers. Lane l holds channels 4 l .. 4 l + 3 (grouped: in the order of the operand's groups).
+  // rows w, w + 8, ..., several at a time so that their loads overlap. Up to 32 rows stay in registers;
+  // more 16-bit ones wait where their operand rows will be (fp32 rows are read again). Lane l holds
+  // channels 4 l .. 4 l + 3 (grouped: in the order of the operand's groups).
   constexpr int kRows = N / 8, kBatch = kRows <= 4 ? kRows : kRows % 4 == 0 ? 4 : 3;
   constexpr bool kKeep = kRows <= 4;
   float qv[kBatch][4] = {};
@@ -358,19 +359,51 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       }
     }
   };
+  auto unpack16 = [&](uint2 x, float (&v)[4]) {
+    if (a.q_dtype == TQ_BF16) {
+      v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
+      v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
+    } else {
+      v[0] = half_lo(x.x); v[1] = half_hi(x.x); v[2] = half_lo(x.y); v[3] = half_hi(x.y);
+    }
+  };
+  const bool stash = !kKeep && a.q_dtype != TQ_F32;
   uint32_t sbits = 0;
   if (warp >= wS && warp < wM) {
     float top2 = 0.f;
     sbits = a.tab->sign_bits[lane >> 3] >> (4 * (lane & 7));
+    if (!kKeep && stash) {
+      constexpr int kAhead = kRows % 8 == 0 ? 8 : 6;
 #pragma unroll 1
-    for (int i0 = 0; i0 < kRows; i0 += kBatch) {
-      load_batch(i0);
+      for (int i0 = 0; i0 < kRows; i0 += kAhead) {
+        uint2 x[kAhead];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const float n2 = warp_sum(qv[i][0] * qv[i][0] + qv[i][1] * qv[i][1] + qv[i][2] * qv[i][2] + qv[i][3] * qv[i][3]);
-        if (n2 < INFINITY) top2 = fmaxf(top2, n2);
+        for (int i = 0; i < kAhead; ++i) {   // rows past the last repeat it
+          const int r = row0 + min((warp - wS) + 8 * (i0 + i), rows - 1), t = r / group;
+          x[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + b * a.qb +
+                                                     a.heads.head[head0 + r - t * group] * a.qh + t * a.qt) + lane);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int r = (warp - wS) + 8 * (i0 + i);
+          *reinterpret_cast<uint2*>(sQ + (r >> 3) * 16 * kcols + (r & 7) * 16 + (lane >> 1) * 128 + (lane & 1) * 8) = x[i];
+          float v[4];
+          unpack16(x[i], v);
+          const float n2 = warp_sum(v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3]);
+          if (n2 < INFINITY) top2 = fmaxf(top2, n2);
+        }
       }
-      if (8 * (i0 + kBatch) >= rows) break;
+    } else {
+#pragma unroll 1
+      for (int i0 = 0; i0 < kRows; i0 += kBatch) {
+        load_batch(i0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const float n2 = warp_sum(qv[i][0] * qv[i][0] + qv[i][1] * qv[i][1] + qv[i][2] * qv[i][2] + qv[i][3] * qv[i][3]);
+          if (n2 < INFINITY) top2 = fmaxf(top2, n2);
+        }
+        if (8 * (i0 + kBatch) >= rows) break;
+      }
     }
     if (lane == 0) ms.norm2[warp - wS] = top2;
   }
@@ -704,7 +737,30 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
 #pragma unroll 1
       for (int i0 = 0; i0 < kRows; i0 += kRot) {
         const int first = (warp - wS) + 8 * i0;
-        if (!kKeep && first < rows) load_batch(i0);
+        if (!kKeep && first < rows) {
+          if (!stash) {
+            load_batch(i0);
+          } else {
+            const uint32_t ch4 = a.mode == TQ_MODE_GROUPED ? *reinterpret_cast<const uint32_t*>(a.tab->chan + 4 * lane) : 0;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int r = first + 8 * i;
+              const uint8_t* row = sQ + (r >> 3) * 16 * kcols + (r & 7) * 16;
+              if (a.mode == TQ_MODE_GROUPED) {
+                uint32_t e[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t ch = (ch4 >> (8 * k)) & 0xffu;
+                  e[k] = *reinterpret_cast<const uint16_t*>(row + (ch >> 3) * 128 + (ch & 7) * 2);
+                }
+                unpack16(make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16)), qv[i]);
+              } else {
+                unpack16(*reinterpret_cast<const uint2*>(row + (lane >> 1) * 128 + (lane & 1) * 8), qv[i]);
+              }
+            }
+            __syncwarp();   // all read before the rows are written over
+          }
+        }
         float v[kRot][4];
 #pragma unroll
         for (int i = 0; i < kRot; ++i)
@@ -951,7 +1007,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       if (both && s == 1) named_sync(3, 256);
     }
     named_sync(3, 256);
-#pragma unroll 2
+#pragma unroll 4
     for (int r = warp - wS; r < rows; r += 8) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);   // no tiles: zeros, or an empty record
       if (nt > 0) v = reinterpret_cast<const float4*>(sV)[r * (kD / 4) + lane];
