@@ -56,8 +56,8 @@ Plan plan_extend(const tq_kv_cache* c, int n_tokens, int n_select, bool listed, 
   const int64_t all = items * c->batch;
   auto splits_of = [&](int b, int T) { return ((one_by_one ? tiles_of(b) : longest) + T - 1) / T; };
   int best_T = longest;
+  double best = 1e300;
   if (all <= kMaxSlots) {
-    double best = 1e300;
     const int most_splits = static_cast<int>(std::min<int64_t>(longest, std::max<int64_t>(4, 3 * sms / all + 1)));
     for (int s = 1; s <= most_splits; ++s) {
       const int T = (longest + s - 1) / s;
@@ -73,6 +73,21 @@ Plan plan_extend(const tq_kv_cache* c, int n_tokens, int n_select, bool listed, 
       if (cost < best) { best = cost; best_T = T; }
     }
   }
+  // More items than SMs leave a last round that few SMs share: run whole rounds of unsplit items, and split
+  // the rest over all SMs (448 items of 120 tiles: three rounds and 4 items split 37 ways, not seven
+  // rounds of halves).
+  a->tail_from = 0x7fffffff;
+  a->tail_splits = 1;
+  const int64_t rest = all % sms;
+  if (one_by_one && all > sms && rest > 0 && rest <= items) {
+    const int last = tiles_of(c->batch - 1), t = std::min<int>(last, sms / static_cast<int>(rest));
+    const double cost = (all / sms) * (longest + kFixedTiles) + (last + t - 1) / t + kFixedTiles + 3.0;
+    if (t > 1 && cost < best && all - rest + rest * t <= kMaxSlots) {
+      best_T = longest;
+      a->tail_from = static_cast<int>(items - rest);
+      a->tail_splits = t;
+    }
+  }
   a->row_tiles = p.row_tiles;
   int64_t blocks = 0;
   if (one_by_one) {
@@ -81,6 +96,7 @@ Plan plan_extend(const tq_kv_cache* c, int n_tokens, int n_select, bool listed, 
       a->splits[b] = static_cast<int16_t>(splits_of(b, best_T));
       blocks += items * a->splits[b];
     }
+    if (a->tail_splits > 1) blocks += rest * (a->tail_splits - 1);
     a->first[c->batch] = static_cast<int>(blocks);
     a->uniform_splits = 1;
   } else {

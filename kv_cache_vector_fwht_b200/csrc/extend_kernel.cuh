@@ -82,6 +82,7 @@ struct ExtendArgs {
   float sketch_ratio;       // rho = sketch_ratio * r16 / n16
   float scale_log2;
   int uniform_splits;       // batch > kMaxList: splits of every sequence
+  int tail_from, tail_splits;   // the last sequence's items from tail_from on have tail_splits splits
   int first[kMaxList + 1];  // first block of threads of each sequence
   int16_t splits[kMaxList];
   HeadLists heads;
@@ -92,8 +93,10 @@ __host__ __device__ constexpr int stream_rows(int n) { return n <= 64 ? n : n / 
 __host__ __device__ constexpr int p_bytes(int n) { return stream_rows(n) / 8 * 2048; }
 // Warpgroups that unpack keys, and as many that unpack values: two each where the softmax threads
 // leave them the registers. One warp unpacks at about 5 cycles an instruction (latencies), so a
-// decode step (N = 16) is bound by it: 131072 tokens x 8 heads took 93 us with one warpgroup each.
-__host__ __device__ constexpr int unpack_groups(int n) { return n <= 32 ? 2 : 1; }
+// decode step (N = 16) is bound by it: 131072 tokens x 8 heads took 93 us with one warpgroup each, 72
+// with two; 35 rows (N = 48) 86 and 73 us. From 64 rows on, where the softmax bounds the kernel and
+// needs 152 registers a thread, two would have 40 each and lose (a prompt's chunk 849 against 957 us).
+__host__ __device__ constexpr int unpack_groups(int n) { return n <= 48 ? 2 : 1; }
 // K, V, 8 softmax, MMA, loader, and 2 warps that fill the last warpgroup
 __host__ __device__ constexpr int block_threads(int n) { return 32 * (8 * unpack_groups(n) + 12); }
 constexpr int kVBytes = kTile * kD * 2;
@@ -296,7 +299,13 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     local = blockIdx.x - b * per;
     n_splits = a.uniform_splits;
   }
-  const int item = local / n_splits, split = local - item * n_splits;
+  int item = local / n_splits, split = local - item * n_splits;
+  if (b == a.batch - 1 && item >= a.tail_from) {   // the launch's last items, more finely split
+    local -= a.tail_from * n_splits;
+    n_splits = a.tail_splits;
+    item = a.tail_from + local / n_splits;
+    split = local % n_splits;
+  }
   const int kv = item % a.n_kv_heads;
   // the last rows see most of a causal context: they start first
   const int rt = a.row_tiles - 1 - item / a.n_kv_heads;
@@ -449,13 +458,14 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
 
   // Registers move from the unpacking and issuing warpgroups to the softmax ones, whose threads hold a
   // logit and a sum for each of their stream's rows:
-  //   48, 64 rows: 256 x 64 + 256 x 152 + 128 x 40 = 60416 of the launch's 640 x 96 = 61440
-  //   32 rows: 512 x 64 + 256 x 96 + 128 x 40 = 62464 of 896 x 72 = 64512
+  //   N >= 64: 256 x 64 + 256 x 152 + 128 x 40 = 60416 of the launch's 640 x 96 = 61440
+  //   N = 48:  512 x 48 + 256 x 128 + 128 x 40 = 62464 of 896 x 72 = 64512
+  //   N = 32:  512 x 64 + 256 x 96 + 128 x 40 = 62464 of 896 x 72
   // A warpgroup changes its share once (a second change would need the warpgroup synchronised in
   // between): what follows the roles is done by the softmax warps.
-  constexpr bool kMove = NS >= 32;
+  constexpr bool kMove = N >= 32;
   if (warp < wV) {
-    if (kMove) reg_dec<64>();
+    if (kMove) reg_dec<N == 48 ? 48 : 64>();
     // ------------------------------------------------------------------ K: thread = token
     const Levels lv0 = load_levels(a.tab, 0), lv1 = load_levels(a.tab, 1);
     const int tok = tid & 127;
@@ -523,7 +533,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       }
     }
   } else if (warp < wS) {
-    if (kMove) reg_dec<64>();
+    if (kMove) reg_dec<N == 48 ? 48 : 64>();
     // ------------------------------------------------------------------ V: thread = token
     const int tok = tid & 127;
     const int o_vq = kTile * (a.idx_bytes + a.sgn_bytes + a.nrm_bytes), o_par = o_vq + kTile * a.vq_bytes;
@@ -716,7 +726,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     }
   } else {
     // ------------------------------------------------------------------ softmax streams
-    if (kMove) reg_inc<NS >= 48 ? 152 : 96>();
+    if (kMove) reg_inc<N == 32 ? 96 : N == 48 ? 128 : 152>();
     const int s = (warp - wS) >> 2, tok = (warp & 3) * 32 + lane;
     uint8_t* myP = sP + s * p_bytes(N);
     float qscale = 1.f;
