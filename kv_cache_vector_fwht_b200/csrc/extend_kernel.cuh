@@ -109,7 +109,7 @@ struct Misc {
   uint64_t raw_full[kMaxStages], raw_empty[kMaxStages];
   uint64_t k_full[kMaxKeyBufs], k_empty[kMaxKeyBufs], v_full[kMaxValueBufs], v_empty[kMaxValueBufs];
   uint64_t s_full[2], p_full[2], p_empty[2];
-  uint64_t rot, sq_in, sq_full, q_full;
+  uint64_t hada, q_in, hada_full, rot, sq_in, sq_full, q_full;
   uint32_t tmem;
   int last;
   int poison[4];            // per value group: lowest position of a non-finite cached value
@@ -162,6 +162,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
 }
+constexpr uint32_t kBf16AB = (1u << 7) | (1u << 10);       // instruction descriptor: A and B bf16
 constexpr uint32_t kMnMajorAB = (1u << 15) | (1u << 16);   // instruction descriptor: A and B M/N-major
 
 // Operand position of rotated coordinate c (the inverse of level_channel) in a run of `bits`-bit codes.
@@ -439,6 +440,9 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       mbar_init(&ms.p_full[i], 4);
       mbar_init(&ms.p_empty[i], 1);
     }
+    mbar_init(&ms.hada, 1);
+    mbar_init(&ms.q_in, 8);
+    mbar_init(&ms.hada_full, 1);
     mbar_init(&ms.rot, 1);
     mbar_init(&ms.sq_in, 8);
     mbar_init(&ms.sq_full, 1);
@@ -543,8 +547,10 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       const uint8_t* raw = sRaw + st.i * a.stage_bytes;
       if (ok) ok = mbar_wait_ns(&ms.raw_full[st.i], st.turn, kWaitNs);
       if (ok && j >= a.value_bufs) ok = mbar_wait_ns(&ms.v_empty[vb.i], vb.turn ^ 1, kWaitNs);
-      // the second buffer holds the sketch matrix until S q has been formed
-      if (ok && j == 1 && prod) ok = mbar_wait_ns(&ms.sq_full, 0, kWaitNs);
+      // until they have been used, the second buffer holds the rotation's matrix and the first the sketch's
+      // (without the former: the second)
+      if (ok && j == 1 && stash) ok = mbar_wait_ns(&ms.hada_full, 0, kWaitNs);
+      if (ok && j == (stash ? 0 : 1) && prod) ok = mbar_wait_ns(&ms.sq_full, 0, kWaitNs);
       const int pos = ms.pos0[j & 15][tok >> 6] + (tok & 63);
       const bool there = pos < len;
       const uint32_t* par = reinterpret_cast<const uint32_t*>(raw + o_par + 16 * tok);
@@ -608,9 +614,13 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     if (kMove) reg_dec<40>();
     if (warp == wL) {
     // ------------------------------------------------------------------ loader
+    if (stash && nt > 0 && lane == 0) {
+      mbar_expect_tx(&ms.hada, kD * kD * 2);
+      bulk_g2s(sV + kVBytes, a.tab->r_umma[a.q_dtype == TQ_BF16], kD * kD * 2, &ms.hada);
+    }
     if (prod && nt > 0 && lane == 0) {
       mbar_expect_tx(&ms.rot, kD * kD * 2);
-      bulk_g2s(sV + kVBytes, a.tab->s_umma, kD * kD * 2, &ms.rot);
+      bulk_g2s(sV + (stash ? 0 : kVBytes), a.tab->s_umma, kD * kD * 2, &ms.rot);
     }
     const int o_sgn = kTile * a.idx_bytes, o_nrm = o_sgn + kTile * a.sgn_bytes, o_vq = o_nrm + kTile * a.nrm_bytes,
               o_par = o_vq + kTile * a.vq_bytes;
@@ -662,15 +672,27 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       const uint32_t qsbo = 16u * kcols;   // bytes of 8 query rows
       const uint64_t q_desc = umma_desc(smem_u32(sQ), 128, qsbo);
       const uint64_t v_desc = umma_desc(smem_u32(sV), 128, 2048), p_desc = umma_desc(smem_u32(sP), 128, 2048);
+      if (stash) {
+        // H (s . q): D [128 x N] = rotation [128 x 128] . q^T, operands of the query's type (+-1: exact)
+        ok = mbar_wait_ns(&ms.hada, 0, kWaitNs);
+        if (ok) ok = mbar_wait_ns(&ms.q_in, 0, kWaitNs);
+        if (ok) {
+          tc_fence_after();
+          const uint32_t id = umma_idesc_f16(128, N) | (a.q_dtype == TQ_BF16 ? kBf16AB : 0u);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) umma_f16(tbase + kS0, v_desc + (kVBytes >> 4) + 16 * k, q_desc + 16 * k, id, k > 0);
+          umma_commit(&ms.hada_full);
+        }
+      }
       if (prod) {
         // S q: D [128 x N] = S_rot [128 x 128] . q'^T, the rows' copy in the sketch's column order
-        ok = mbar_wait_ns(&ms.rot, 0, kWaitNs);
+        if (ok) ok = mbar_wait_ns(&ms.rot, 0, kWaitNs);
         if (ok) ok = mbar_wait_ns(&ms.sq_in, 0, kWaitNs);
         if (ok) {
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 8; ++k)   // 16 columns a step: two core matrices of 128 bytes
-            umma_f16(tbase + kS0, v_desc + (kVBytes >> 4) + 16 * k, p_desc + 16 * k, umma_idesc_f16(128, N), k > 0);
+            umma_f16(tbase + kS0, v_desc + (stash ? 0 : kVBytes >> 4) + 16 * k, p_desc + 16 * k, umma_idesc_f16(128, N), k > 0);
           umma_commit(&ms.sq_full);
         }
       }
@@ -740,99 +762,103 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       qscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       const float unit = down * (a.mode == TQ_MODE_GROUPED ? 0.17677669529663688f : 0.08838834764831845f);
-      const int last_stage = a.mode == TQ_MODE_GROUPED ? 4 : 16;   // grouped: 32-point blocks
-      // kRot rows at a time: many rows for the overlap of their shuffles, one at a time (and less code to
-      // fetch) where there are few
-      constexpr int kRot = kKeep ? 1 : kBatch;
+      if (stash) {
+        // many 16-bit rows: on the tensor cores, which read them where the operand will be; a thread then
+        // holds coordinate tok of its stream's half of the rows
+        fence_async_smem();
+        warp_arrive(&ms.q_in, lane);
+        ok = mbar_wait_ns(&ms.hada_full, 0, kWaitNs);
+        tc_fence_after();
+        const bool rest = a.mode == TQ_MODE_GROUPED && tok >= 32;
+        const int k = rest ? 32 + operand_position(a.bits1, tok - 32) : operand_position(a.bits0, tok);
+        const int k2 = tok < 64 ? 2 * tok : 2 * (tok - 64) + 1;   // the sketch matrix's column order
+        constexpr int kCols = (N / 2 + 15) / 16 * 16;
 #pragma unroll 1
-      for (int i0 = 0; i0 < kRows; i0 += kRot) {
-        const int first = (warp - wS) + 8 * i0;
-        if (!kKeep && first < rows) {
-          if (!stash) {
-            load_batch(i0);
-          } else {
-            const uint32_t ch4 = a.mode == TQ_MODE_GROUPED ? *reinterpret_cast<const uint32_t*>(a.tab->chan + 4 * lane) : 0;
+        for (int c = s * kCols; c < min(N, (s + 1) * kCols); c += 16) {
+          uint32_t x[16];
+          tmem_ld16_sync(tlane + kS0 + c, x);
+          uint8_t* col = sQ + (c >> 3) * 16 * kcols + (k >> 3) * 128 + (k & 7) * 2;
+          uint8_t* pcol = sP + (c >> 3) * 2048 + (k2 >> 3) * 128 + (k2 & 7) * 2;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int r = first + 8 * i;
-              const uint8_t* row = sQ + (r >> 3) * 16 * kcols + (r & 7) * 16;
-              if (a.mode == TQ_MODE_GROUPED) {
-                uint32_t e[4];
+          for (int i = 0; i < 16; ++i) {
+            const __half h = __float2half_rn(__uint_as_float(x[i]) * unit);
+            *reinterpret_cast<__half*>(col + (i >> 3) * 16 * kcols + (i & 7) * 16) = h;
+            if (prod) *reinterpret_cast<__half*>(pcol + (i >> 3) * 2048 + (i & 7) * 16) = h;
+          }
+        }
+        tc_fence_before();
+      } else {
+        const int last_stage = a.mode == TQ_MODE_GROUPED ? 4 : 16;   // grouped: 32-point blocks
+        // kRot rows at a time: many rows for the overlap of their shuffles, one at a time (and less code to
+        // fetch) where there are few
+        constexpr int kRot = kKeep ? 1 : kBatch;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kRows; i0 += kRot) {
+          const int first = (warp - wS) + 8 * i0;
+          if (!kKeep && first < rows) load_batch(i0);
+          float v[kRot][4];
+#pragma unroll
+          for (int i = 0; i < kRot; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v[i][k] = qv[i][k];
+#pragma unroll
+              for (int n = 1; kKeep && n < kBatch; ++n) v[i][k] = i0 == n ? qv[n][k] : v[i][k];
+              v[i][k] = flip_sign(v[i][k] * unit, sbits, k);
+            }
+          if (first < rows) {
+#pragma unroll
+            for (int i = 0; i < kRot; ++i) fwht_reg<4>(v[i]);
+#pragma unroll
+            for (int m = 1; m <= 16; m <<= 1) {
+              if (m > last_stage) break;
+#pragma unroll
+              for (int i = 0; i < kRot; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const uint32_t ch = (ch4 >> (8 * k)) & 0xffu;
-                  e[k] = *reinterpret_cast<const uint16_t*>(row + (ch >> 3) * 128 + (ch & 7) * 2);
+                  const float o = __shfl_xor_sync(kFull, v[i][k], m);
+                  v[i][k] = lane & m ? o - v[i][k] : v[i][k] + o;
                 }
-                unpack16(make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16)), qv[i]);
-              } else {
-                unpack16(*reinterpret_cast<const uint2*>(row + (lane >> 1) * 128 + (lane & 1) * 8), qv[i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kRot; ++i) {
+            const int r = first + 8 * i;
+            uint8_t* qrow = sQ + (r >> 3) * 16 * kcols + (r & 7) * 16;
+            uint8_t* prow = sP + (r >> 3) * 2048 + (r & 7) * 16;   // in the sketch matrix's column order
+            if (r >= rows) {   // zeros: no row, no score above its reference
+              if (lane < 16) {
+                *reinterpret_cast<uint4*>(qrow + 128 * lane) = make_uint4(0, 0, 0, 0);
+                if (prod) *reinterpret_cast<uint4*>(prow + 128 * lane) = make_uint4(0, 0, 0, 0);
+              }
+              continue;
+            }
+            const uint32_t h01 = h2bits(__floats2half2_rn(v[i][0], v[i][1])), h23 = h2bits(__floats2half2_rn(v[i][2], v[i][3]));
+            if (a.mode != TQ_MODE_GROUPED && a.bits0 >= 3) {   // the operand's order is the coordinates'
+              *reinterpret_cast<uint2*>(qrow + (lane >> 1) * 128 + (lane & 1) * 8) = make_uint2(h01, h23);
+            } else {
+#pragma unroll
+              for (int k4 = 0; k4 < 4; ++k4) {
+                const int c = 4 * lane + k4;
+                const bool rest = a.mode == TQ_MODE_GROUPED && c >= 32;
+                const int k = rest ? 32 + operand_position(a.bits1, c - 32) : operand_position(a.bits0, c);
+                *reinterpret_cast<uint16_t*>(qrow + (k >> 3) * 128 + (k & 7) * 2) =
+                    static_cast<uint16_t>((k4 < 2 ? h01 : h23) >> (16 * (k4 & 1)));
               }
             }
-            __syncwarp();   // all read before the rows are written over
-          }
-        }
-        float v[kRot][4];
-#pragma unroll
-        for (int i = 0; i < kRot; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            v[i][k] = qv[i][k];
-#pragma unroll
-            for (int n = 1; kKeep && n < kBatch; ++n) v[i][k] = i0 == n ? qv[n][k] : v[i][k];
-            v[i][k] = flip_sign(v[i][k] * unit, sbits, k);
-          }
-        if (first < rows) {
-#pragma unroll
-          for (int i = 0; i < kRot; ++i) fwht_reg<4>(v[i]);
-#pragma unroll
-          for (int m = 1; m <= 16; m <<= 1) {
-            if (m > last_stage) break;
-#pragma unroll
-            for (int i = 0; i < kRot; ++i)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float o = __shfl_xor_sync(kFull, v[i][k], m);
-                v[i][k] = lane & m ? o - v[i][k] : v[i][k] + o;
-              }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kRot; ++i) {
-          const int r = first + 8 * i;
-          uint8_t* qrow = sQ + (r >> 3) * 16 * kcols + (r & 7) * 16;
-          uint8_t* prow = sP + (r >> 3) * 2048 + (r & 7) * 16;   // in the sketch matrix's column order
-          if (r >= rows) {   // zeros: no row, no score above its reference
-            if (lane < 16) {
-              *reinterpret_cast<uint4*>(qrow + 128 * lane) = make_uint4(0, 0, 0, 0);
-              if (prod) *reinterpret_cast<uint4*>(prow + 128 * lane) = make_uint4(0, 0, 0, 0);
+            if (prod) {   // columns c, c + 64 side by side: lane l < 16 pairs up with lane l + 16
+              const uint32_t o01 = __shfl_xor_sync(kFull, h01, 16), o23 = __shfl_xor_sync(kFull, h23, 16);
+              if (lane < 16)
+                *reinterpret_cast<uint4*>(prow + 128 * lane) = make_uint4(prmt(h01, o01, 0x5410), prmt(h01, o01, 0x7632),
+                                                                          prmt(h23, o23, 0x5410), prmt(h23, o23, 0x7632));
             }
-            continue;
-          }
-          const uint32_t h01 = h2bits(__floats2half2_rn(v[i][0], v[i][1])), h23 = h2bits(__floats2half2_rn(v[i][2], v[i][3]));
-          if (a.mode != TQ_MODE_GROUPED && a.bits0 >= 3) {   // the operand's order is the coordinates'
-            *reinterpret_cast<uint2*>(qrow + (lane >> 1) * 128 + (lane & 1) * 8) = make_uint2(h01, h23);
-          } else {
-#pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-              const int c = 4 * lane + k4;
-              const bool rest = a.mode == TQ_MODE_GROUPED && c >= 32;
-              const int k = rest ? 32 + operand_position(a.bits1, c - 32) : operand_position(a.bits0, c);
-              *reinterpret_cast<uint16_t*>(qrow + (k >> 3) * 128 + (k & 7) * 2) =
-                  static_cast<uint16_t>((k4 < 2 ? h01 : h23) >> (16 * (k4 & 1)));
-            }
-          }
-          if (prod) {   // columns c, c + 64 side by side: lane l < 16 pairs up with lane l + 16
-            const uint32_t o01 = __shfl_xor_sync(kFull, h01, 16), o23 = __shfl_xor_sync(kFull, h23, 16);
-            if (lane < 16)
-              *reinterpret_cast<uint4*>(prow + 128 * lane) = make_uint4(prmt(h01, o01, 0x5410), prmt(h01, o01, 0x7632),
-                                                                        prmt(h23, o23, 0x5410), prmt(h23, o23, 0x7632));
           }
         }
       }
       fence_async_smem();
       if (prod) {
         warp_arrive(&ms.sq_in, lane);
-        ok = mbar_wait_ns(&ms.sq_full, 0, kWaitNs);
+        if (ok) ok = mbar_wait_ns(&ms.sq_full, 0, kWaitNs);
         tc_fence_after();
         // lane = sketch row j; a stream's warps take half of the query rows
         const int k = kD + operand_position(1, tok);

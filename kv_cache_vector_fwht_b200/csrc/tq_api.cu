@@ -264,6 +264,16 @@ static tq_status build_quantizer(int d, int bits, int mode, uint64_t seed,
       }
   }
   if (mode == TQ_MODE_GROUPED) gather_schedule(q->host.chan, h->gsched);
+  for (int j = 0; j < kD; ++j)
+    for (int p = 0; p < kD; ++p) {   // coordinate j of the rotated row, position p of the group order
+      const bool block = mode != TQ_MODE_GROUPED || (j >> 5) == (p >> 5);
+      const int bits = mode == TQ_MODE_GROUPED ? (j & p & 31) : (j & p);
+      const bool neg = (__builtin_popcount(bits) & 1) != (q->host.signs[p] < 0);
+      const int c = q->host.chan[p];
+      const size_t off = static_cast<size_t>(j >> 3) * 1024 + (c >> 3) * 64 + (j & 7) * 8 + (c & 7);
+      h->r_umma[0][off] = !block ? 0 : neg ? 0xbc00 : 0x3c00;
+      h->r_umma[1][off] = !block ? 0 : neg ? 0xbf80 : 0x3f80;
+    }
   const int bits0 = mode == TQ_MODE_PROD ? bits - 1 : mode == TQ_MODE_GROUPED ? bits + 1 : bits;
   h->lv_scale[0] = q->lv_scale[0] = level_bytes(q->host.cent[0], bits0, h->lv_lo[0], h->lv_hi[0]);
   if (mode == TQ_MODE_GROUPED)

@@ -32,6 +32,9 @@ struct DevTables {
   // k' = 2p holds column p and k' = 2p + 1 column p + 64, laid out in the canonical K-major
   // no-swizzle form (element (j, k') at byte (j/8)*2048 + (k'/8)*128 + (j%8)*16 + (k'%8)*2).
   alignas(16) uint16_t s_umma[kD * kD];
+  // the rotation H diag(s) (grouped: the channel order and the 32-point blocks with it; entries +-1 and 0) as
+  // a tensor-core A operand in the same form, columns in channel order: [0] fp16, [1] bf16
+  alignas(16) uint16_t r_umma[2][kD * kD];
   // rotation signs of bf16 element pairs: word q has bit 15 set if s_{2q} = -1, bit 31 if
   // s_{2q+1} = -1 (an XOR flips both elements of a packed pair).
   alignas(16) uint32_t pair_mask[kD / 2];
