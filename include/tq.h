@@ -346,7 +346,7 @@ tq_status tq_norm_rope(const tq_rope* rope, int dtype, int batch, int n_tokens, 
  * on 16-bit tensor-core operands with 32-bit sums: rotated queries, centroids, softmax weights
  * and dequantised values are rounded to fp16 (relative 2^-11 each), the softmax statistics
  * and outputs are held in fp32. Non-finite cached rows reach only the query rows that attend
- * to them. n_tokens = 0 is a no-op.
+ * to them. n_tokens = 0 is a no-op; n_q_heads * n_tokens up to 2^30.
  *
  * Workspace (this call, tq_select_blocks and tq_decode_attention_blocks): zero-filled before
  * its first use, 16-byte aligned; every call leaves it reusable by any of the three, whatever

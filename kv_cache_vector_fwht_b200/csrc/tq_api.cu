@@ -621,6 +621,7 @@ tq_status tq_extend_attention(const tq_quantizer* q, const tq_kv_cache* c, tq_he
   if (c->value_bits == 0 || n_tokens < 0) return TQ_EINVAL;
   if (!known_dtype(q_dtype) || !known_dtype(out_dtype)) return TQ_EUNSUPPORTED;
   if (n_tokens == 0) return TQ_OK;
+  if (static_cast<int64_t>(n_q_heads) * n_tokens > (1 << 30)) return TQ_EUNSUPPORTED;   // rows are counted in 32 bits
   if ((st = check_view(query, q_dtype, c->batch, n_q_heads, n_tokens)) != TQ_OK) return st;
   if ((st = check_view(out, out_dtype, c->batch, n_q_heads, n_tokens)) != TQ_OK) return st;
   if ((st = check_space(workspace, workspace_bytes, kWorkspaceHeader + extend_scratch_bytes(c, n_q_heads, n_tokens))) != TQ_OK)

@@ -100,6 +100,7 @@ def test_norm_rope_unused_side_and_unturned_rows_need_no_pointers():
     (dict(map=[0, 1, 1, 1]), ECUDA),
     (dict(n=-1), EINVAL),
     (dict(n=0), OK),
+    (dict(n=1 << 29), EUNSUP),
     (dict(qdt=5), EUNSUP),
     (dict(odt=5), EUNSUP),
     (dict(qdt=F16, odt=F32), ECUDA),

@@ -84,6 +84,19 @@ def test_types_and_query_sizes(q_dtype, out_dtype, size):
     check(extend(qg, cache, q, out_dtype), ref, tol, out_dtype)
 
 
+@pytest.mark.parametrize("q_dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("mode,bits", [("prod", 3), ("grouped", 1), ("mse", 2)])
+@pytest.mark.parametrize("group,n", [(5, 5), (4, 11), (12, 5), (30, 3), (13, 10)])
+def test_types_at_many_rows(q_dtype, mode, bits, group, n):
+    """25, 44, 60, 90 and 130 rows of each query type: rows of 16 bits and of 32 are rotated in different ways."""
+    require_cuda()
+    lengths = [190]
+    qo, qg, oc, cache, g = make_case(17, mode, bits, 4, lengths, 1, 192)
+    q = query_rows(g, (1, group, n, 128), q_dtype)
+    ref, tol = attention64(qo, oc, q.double().numpy(), causal_limits(lengths, n), 4)
+    check(extend(qg, cache, q, F32), ref, tol, F32)
+
+
 def test_strided_queries_and_outputs():
     """A projection's (batch, tokens, heads, d) rows as a view, and an output inside a larger one whose
     other elements stay as they are."""
@@ -174,6 +187,45 @@ def test_stale_rows_and_later_tokens_do_not_reach_a_row():
             assert out[0, h, 2].isnan().all()
             out[0, h, 2] = torch.from_numpy(without[0, h, 2]).float()
     check(out, without, wtol, F32)
+
+
+@pytest.mark.parametrize("group,n", [(2, 2), (6, 9)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_query_row_that_is_not_finite_spoils_no_other(group, n, dtype):
+    require_cuda()
+    lengths = [140]
+    qo, qg, oc, cache, g = make_case(18, "prod", 4, 2, lengths, 1, 144)
+    q = query_rows(g, (1, group, n, 128), dtype)
+    ref, tol = attention64(qo, oc, q.double().numpy(), causal_limits(lengths, n), 2)
+    q[0, 0, 0, 3], q[0, 1, 1, 7] = float("inf"), float("nan")
+    out = extend(qg, cache, q, F32)
+    for h, t in ((0, 0), (1, 1)):
+        assert out[0, h, t].isnan().all()
+        out[0, h, t] = torch.from_numpy(ref[0, h, t]).float()
+    check(out, ref, tol, F32)
+
+
+def test_many_items_with_a_split_last_round():
+    """More tiles of query rows than SMs: whole rounds, and the last few tiles shared by all SMs."""
+    require_cuda()
+    n = 128 * 150
+    qo, qg, oc, cache, g = make_case(19, "mse", 2, 2, [n], 1, n)
+    q = query_rows(g, (1, 1, n, 128), BF16)
+    some = [0, 1, 127, 128, 255, 256, 9600, 12345, n - 2, n - 1]
+    ref, tol = attention64(qo, oc, q[:, :, some].float().numpy(), [[t + 1 for t in some]], 2)
+    out = extend(qg, cache, q, F32)
+    check(out[:, :, some], ref, tol, F32)
+    assert out.isfinite().all()
+
+
+def test_many_long_sequences():
+    """Over 64 sequences, each in several splits."""
+    require_cuda()
+    lengths = [1500 - 20 * i for i in range(66)]
+    qo, qg, oc, cache, g = make_case(20, "mse", 2, 2, lengths, 1, 1504)
+    q = query_rows(g, (66, 1, 2, 128), BF16)
+    ref, tol = attention64(qo, oc, q.float().numpy(), causal_limits(lengths, 2), 2)
+    check(extend(qg, cache, q, F32), ref, tol, F32)
 
 
 def test_many_sequences():
