@@ -129,6 +129,7 @@ class Rope(ctypes.Structure):
 
 
 _NO_HEADS = Heads(None, 0, 0, 0)
+_D_SHAPE = (D,)
 
 
 _lib.tq_norm_rope.argtypes = [POINTER(Rope), c_int, c_int, c_int, c_int, c_int, Heads, Heads,
@@ -517,47 +518,58 @@ def tq_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weigh
     fp32, rot_dim / 2 entries on the device. axis_of_freq: the axis each of them reads (host
     sequence; None: axis 0). q_weight / k_weight: 128 norm weights each, in the tensors' type. norm:
     whether to normalise; None: if a weight is given."""
+    import torch
     x = q if q is not None else k
-    _require(x is not None and x.dim() == 4, "tq_norm_rope: q or k is needed, (batch, heads, n_tokens, 128)")
+    if x is None or x.dim() != 4:
+        raise ValueError("tq_norm_rope: q or k is needed, (batch, heads, n_tokens, 128)")
     batch, _, n_tokens, _ = x.shape
-    dtype, dev = x.dtype, x.device
-    args = []
-    for a, o, w in ((q, q_out, q_weight), (k, k_out, k_weight)):
-        if a is None:
-            _require(o is None, "tq_norm_rope: an output without its input")
-            args += (0, _NO_HEADS, _NO_HEADS, None)
-            continue
-        shape = a.shape
-        if not (o is not None and o.shape == shape and len(shape) == 4 and shape[0] == batch
-                and shape[2] == n_tokens and shape[3] == D):
-            raise ValueError("tq_norm_rope: tensors are (batch, heads, n_tokens, 128), outputs as their inputs")
-        if not (a.dtype == dtype and o.dtype == dtype and a.device == dev and o.device == dev):
-            raise ValueError("tq_norm_rope: one type and one device for all tensors")
-        si, so = a.stride(), o.stride()
-        if si[3] != 1 or so[3] != 1:
-            raise ValueError("tq_norm_rope: channels must be adjacent")
-        if w is not None and not (w.dtype == dtype and w.shape == (D,) and w.is_contiguous() and w.device == dev):
-            raise ValueError("tq_norm_rope: weights are 128 contiguous values of the tensors' type")
-        args += (shape[1], Heads(a.data_ptr(), si[0], si[1], si[2]), Heads(o.data_ptr(), so[0], so[1], so[2]),
-                 _ptr(w))
+    dtype, dev = x.dtype, x.get_device()
+    q_args = _rope_side(q, q_out, q_weight, batch, n_tokens, dtype, dev)
+    k_args = _rope_side(k, k_out, k_weight, batch, n_tokens, dtype, dev)
     pshape = positions.shape
-    if not (str(positions.dtype) == "torch.int32" and positions.is_contiguous() and len(pshape) in (2, 3)
+    if not (positions.dtype == torch.int32 and positions.is_contiguous() and len(pshape) in (2, 3)
             and pshape[-2] == batch and pshape[-1] == n_tokens):
         raise ValueError("tq_norm_rope: positions are int32 (n_axes, batch, n_tokens), contiguous")
-    if not (inv_freq.dim() == 1 and inv_freq.is_contiguous() and _dtype_code(inv_freq) == TQ_F32):
+    if not (inv_freq.dim() == 1 and inv_freq.dtype == torch.float32 and inv_freq.is_contiguous()):
         raise ValueError("tq_norm_rope: inv_freq is a contiguous fp32 vector")
     _on_current_device("tq_norm_rope", x, positions, inv_freq)
     pairs = inv_freq.shape[0]
     axes = None
     if axis_of_freq is not None:
-        _require(len(axis_of_freq) == pairs, "tq_norm_rope: one axis per frequency")
+        if len(axis_of_freq) != pairs:
+            raise ValueError("tq_norm_rope: one axis per frequency")
         axes = bytes(axis_of_freq)
     rope = Rope(positions.data_ptr(), inv_freq.data_ptr(), axes, pshape[0] if len(pshape) == 3 else 1,
-                2 * pairs, int(interleaved))
+                2 * pairs, interleaved)
     if norm is None:
         norm = q_weight is not None or k_weight is not None
-    _check(_lib.tq_norm_rope(ctypes.byref(rope), _dtype_code(x), batch, n_tokens, D, *args, int(norm), eps,
-                             _stream(stream)), "tq_norm_rope")
+    st = _lib.tq_norm_rope(ctypes.byref(rope), _dtype_code(x), batch, n_tokens, D, *q_args, *k_args, norm, eps,
+                           _stream(stream))
+    if st != TQ_OK:
+        _check(st, "tq_norm_rope")
+
+
+def _rope_side(a, o, w, batch, n_tokens, dtype, dev):
+    """Head count, input and output views and weights of one side of tq_norm_rope, checked."""
+    if a is None:
+        _require(o is None, "tq_norm_rope: an output without its input")
+        return 0, _NO_HEADS, _NO_HEADS, None
+    shape = a.shape
+    if o is None or o.shape != shape or len(shape) != 4 or shape[0] != batch or shape[2] != n_tokens or shape[3] != D:
+        raise ValueError("tq_norm_rope: tensors are (batch, heads, n_tokens, 128), outputs as their inputs")
+    if a.dtype != dtype or o.dtype != dtype or a.get_device() != dev or o.get_device() != dev:
+        raise ValueError("tq_norm_rope: one type and one device for all tensors")
+    sb, sh, st, sd = a.stride()
+    ob, oh, ot, od = o.stride()
+    if sd != 1 or od != 1:
+        raise ValueError("tq_norm_rope: channels must be adjacent")
+    if w is None:
+        pw = None
+    elif w.dtype == dtype and w.shape == _D_SHAPE and w.is_contiguous() and w.get_device() == dev:
+        pw = w.data_ptr()
+    else:
+        raise ValueError("tq_norm_rope: weights are 128 contiguous values of the tensors' type")
+    return shape[1], Heads(a.data_ptr(), sb, sh, st), Heads(o.data_ptr(), ob, oh, ot), pw
 
 
 def tq_extend_workspace_bytes(cache: KVCache, n_q_heads: int, n_tokens: int) -> int:
