@@ -9,18 +9,20 @@ namespace tq {
 namespace {
 
 // ------------------------------------------------------------------------------- bounds
-// min and max over a block's tokens of n16 c[idx_j] / sqrt(d), channel by channel. A block of threads
-// walks a few token blocks of one (sequence, KV head); thread = (word of the row, every G-th token):
-// it unpacks its index words to fp16 levels, scales them by the token's norm in fp32 and keeps the
-// channels' minimum and maximum in registers, the next block's rows being loaded meanwhile. Then the
-// threads that share a word are joined in fp16, the type of the result (rounding is monotone, so
-// the minimum of the rounded is the rounded minimum): by exchanges within the warp, where the row's
-// words divide it, and in shared memory.
-// Bound by instructions: a value costs a conversion, a product and a share of two three-way minima
-// beside its lookup, against half a byte read: 35 us for 8 x 4 x 20000 rows of 2-bit codes (36 bytes
-// a row read, 31 MB), where HBM alone would take 5. Packed fp16 products are no faster to speak of (34
-// us) and half as far again from the exact bounds.
-constexpr int kBT = 128;
+// min and max over a block's tokens of n16 c[idx_j] / sqrt(d), channel by channel. Rounding to fp16, the
+// type of the result, is monotone: the minimum of the rounded products is the rounded minimum. So a
+// token's products with the whole codebook are made first (fp32, one rounding: 4 products of a 2-bit
+// codebook, 8 of a 3-bit one, the 8 positive ones of a 4-bit one), as byte pools like the codebook's
+// own; the token's codes then look up finished fp16 numbers, two to a register, and a value costs its
+// lookup and half a minimum and half a maximum. A warp takes a few token blocks of one (sequence, KV
+// head): its lanes make the pools of two rows each, then lane = (word of the row, every G-th row) with
+// its channels' minima and maxima in registers. The next block's words are loaded before this block's
+// results are joined. The lanes that share a word are joined at the end, by exchanges where the row's words
+// divide the warp and in shared memory otherwise.
+// Bound by instructions of the ALU pipe (lookups, minima): 8 sequences of 8192 to 32768 rows x 4
+// KV heads of 2-bit codes (36 bytes a row read, 31 MB) take 17 us, where HBM alone would take 5. With the
+// conversions and products of every value in fp32 it was 38.
+constexpr int kBW = 4;   // warps of a block of threads
 
 struct BoundsArgs {
   const uint8_t* idx;
@@ -28,29 +30,60 @@ struct BoundsArgs {
   const int32_t* len;
   __half* bounds;
   const DevTables* tab;
-  int n_kv_heads, capacity, n_tokens, n_blocks, per_cta, n_norms;
+  int n_kv_heads, capacity, n_tokens, n_blocks, per_warp, n_norms;
   float scale0, scale1;  // level scale / sqrt(channels of the group)
 };
 
-// Minima lo and maxima hi of one word's channels over R rows (their index words and score factors).
-template <int BITS, int R>
-__device__ __forceinline__ void bounds_step(const uint32_t (&w)[R], const float (&f)[R], const Levels& lv, float* lo, float* hi) {
-  constexpr int NP = level_pairs(BITS);
+// Two fp16 levels (low bytes in lo, high bytes in hi, selected by sel) times f, rounded once.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t lo, uint32_t hi, uint32_t sel, float f) {
+  const uint32_t y = prmt(lo, hi, sel);
+  const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&y));
+  const __half2 r = __floats2half2_rn(l.x * f, l.y * f);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The pools of a codebook's products with f.
+template <int BITS>
+__device__ __forceinline__ void scale_levels(const Levels& lv, float f, uint4* dst) {
+  if constexpr (BITS == 1) {
+    const uint32_t y = scaled_pair(lv.lo[0], 0, 0x3210, f);
+    *reinterpret_cast<uint32_t*>(dst) = y;
+  } else if constexpr (BITS == 2) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(scaled_pair(lv.lo[0], 0, 0x3210, f), scaled_pair(lv.lo[1], 0, 0x3210, f));
+  } else {
+    uint32_t o[4];
 #pragma unroll
-  for (int u = 0; u < R; u += 2) {   // two rows a step: a three-way minimum takes both
-    uint32_t y0[NP], y1[NP];
-    unpack_levels<BITS>(w[u], lv, y0);
-    unpack_levels<BITS>(w[u + 1], lv, y1);
-    const uint64_t f0 = pk2(f[u], f[u]), f1 = pk2(f[u + 1], f[u + 1]);
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(&y0[i])), l1 = __half22float2(*reinterpret_cast<const __half2*>(&y1[i]));
-      const float2 a0 = up2(mul2(pk2(l0.x, l0.y), f0)), a1 = up2(mul2(pk2(l1.x, l1.y), f1));
-      lo[2 * i] = min3(lo[2 * i], a0.x, a1.x);
-      hi[2 * i] = max3(hi[2 * i], a0.x, a1.x);
-      lo[2 * i + 1] = min3(lo[2 * i + 1], a0.y, a1.y);
-      hi[2 * i + 1] = max3(hi[2 * i + 1], a0.y, a1.y);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t y0 = scaled_pair(lv.lo[i], lv.hi[i], 0x5140, f), y1 = scaled_pair(lv.lo[i], lv.hi[i], 0x7362, f);
+      o[2 * i] = prmt(y0, y1, 0x6420);
+      o[2 * i + 1] = prmt(y0, y1, 0x7531);
     }
+    *dst = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+template <int BITS>
+__device__ __forceinline__ Levels scaled_levels(const uint4* src) {
+  if constexpr (BITS == 1) return Levels{{*reinterpret_cast<const uint32_t*>(src), 0}, {0, 0}};
+  if constexpr (BITS == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(src);
+    return Levels{{v.x, v.y}, {0, 0}};
+  }
+  const uint4 v = *src;
+  return Levels{{v.x, v.z}, {v.y, v.w}};
+}
+
+// Two rows' words into the minima and maxima (one three-way minimum takes both).
+template <int BITS, int N>
+__device__ __forceinline__ void bounds_rows(uint32_t w0, uint32_t w1, const uint4* pool0, const uint4* pool1, __half2 (&v)[N]) {
+  constexpr int NP = level_pairs(BITS);
+  uint32_t y0[NP], y1[NP];
+  unpack_levels<BITS>(w0, scaled_levels<BITS>(pool0), y0);
+  unpack_levels<BITS>(w1, scaled_levels<BITS>(pool1), y1);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const __half2 a = *reinterpret_cast<const __half2*>(&y0[i]), b = *reinterpret_cast<const __half2*>(&y1[i]);
+    v[i] = __hmin2(__hmin2(v[i], a), b);
+    v[N / 2 + i] = __hmax2(__hmax2(v[N / 2 + i], a), b);
   }
 }
 
@@ -60,110 +93,137 @@ __device__ __forceinline__ void join_lanes(__half2* v, int lane) {
   const bool up = lane & M;
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) {
-    const __half2 mine = up ? v[i + N / 2] : v[i], theirs = up ? v[i] : v[i + N / 2];
+    const __half2 a = v[i], b = v[i + N / 2];
+    const __half2 mine = up ? b : a, theirs = up ? a : b;
     v[i] = __hmin2(mine, __shfl_xor_sync(kFull, theirs, M));
   }
 }
 
 // B0, B1: code bits of the two channel groups (B1 = 0: one group).
 template <int B0, int B1>
-__global__ void __launch_bounds__(kBT, B0 == 1 || B1 == 1 ? 4 : 6) k_block_bounds(const __grid_constant__ BoundsArgs a) {
+__global__ void __launch_bounds__(32 * kBW, B0 == 2 && B1 == 0 ? 8 : 5) k_block_bounds(const __grid_constant__ BoundsArgs a) {
   constexpr bool kGrouped = B1 != 0;
+  constexpr int B1x = kGrouped ? B1 : B0;
   constexpr int kWords0 = (kGrouped ? 1 : 4) * storage_width_c(B0);               // 32-bit words of the first group
-  constexpr int kWords = kWords0 + (kGrouped ? 3 * storage_width_c(kGrouped ? B1 : 1) : 0);
-  constexpr int kGroups = kBT / kWords;      // threads that share a word
-  constexpr int kR = kWords <= 5 ? 2 : 4;    // rows in flight
-  constexpr int kSteps = (TQ_BLOCK + kR * kGroups - 1) / (kR * kGroups);
-  constexpr int NP0 = level_pairs(B0), NP1 = kGrouped ? level_pairs(kGrouped ? B1 : 1) : 1, NP = NP0 > NP1 ? NP0 : NP1;
-  constexpr int kParts = kGrouped ? kGroups : kBT / 32;
-  __shared__ __align__(16) __half2 part[kParts][2][kD / 2];   // minima and negated maxima to be joined
-  __shared__ __half res[2][kD];
-  const int b = blockIdx.z, kv = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  constexpr int kWords = kWords0 + (kGrouped ? 3 * storage_width_c(B1x) : 0);
+  constexpr int kGroups = 32 / kWords;                                            // lanes that share a word
+  constexpr int kRows = (TQ_BLOCK + kGroups - 1) / kGroups;                       // a lane's rows of a block
+  constexpr int NP0 = level_pairs(B0), NP1 = level_pairs(B1x), NP = NP0 > NP1 ? NP0 : NP1;
+  __shared__ uint4 pools[kBW][kGrouped ? 2 : 1][TQ_BLOCK];
+  __shared__ __align__(16) __half2 parts[kBW][kGrouped ? kGroups : 1][2][kD / 2];   // grouped: minima and negated maxima to be joined
+  __shared__ __align__(16) __half res_all[kBW][2][kD];
+  const int b = blockIdx.z, kv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = min(a.len[b], a.capacity);
-  const int blk0 = max(0, len - a.n_tokens) / TQ_BLOCK + blockIdx.x * a.per_cta;
+  const int blk0 = max(0, len - a.n_tokens) / TQ_BLOCK + (blockIdx.x * kBW + warp) * a.per_warp;
   const int n_rows = len - blk0 * TQ_BLOCK;
   if (n_rows <= 0) return;
-  const int blocks = min(a.per_cta, (n_rows + TQ_BLOCK - 1) / TQ_BLOCK);
+  const int blocks = min(a.per_warp, (n_rows + TQ_BLOCK - 1) / TQ_BLOCK);
   const int64_t pair = static_cast<int64_t>(b) * a.n_kv_heads + kv;
   const int64_t row0 = pair * a.capacity + static_cast<int64_t>(blk0) * TQ_BLOCK;
-  const int word = tid % kWords, g = tid / kWords;
-  __half2* out = reinterpret_cast<__half2*>(a.bounds + (pair * a.n_blocks + blk0) * 2 * kD);
+  // the few lanes beyond groups x words repeat the last group's rows
+  const int word = lane % kWords, g = min(lane / kWords, kGroups - 1);
   const bool second = kGrouped && word >= kWords0;
-  const Levels lv = load_levels(a.tab, second);
-  const float scale = second ? a.scale1 : a.scale0;
+  const Levels lv0 = load_levels(a.tab, 0), lv1 = load_levels(a.tab, kGrouped ? 1 : 0);
   const int n_norms = kGrouped ? 2 : a.n_norms;   // prod rows hold ||r|| too
   const uint32_t* words = reinterpret_cast<const uint32_t*>(a.idx) + row0 * kWords + word;
-  const uint16_t* norms = a.norms + row0 * n_norms + second;
-  uint32_t w[kR];
-  uint16_t nr[kR];
-  // rows of step `it`; a row seen twice changes no minimum (nor do the few threads beyond groups x words)
-  auto load = [&](int it) {
-    const int first = it / kSteps * TQ_BLOCK, last = min(n_rows, first + TQ_BLOCK) - 1;
+  const uint16_t* norms = a.norms + row0 * n_norms;
+  uint4 (*pool)[TQ_BLOCK] = pools[warp];
+  __half* res = &res_all[warp][0][0];
+  uint4* out = reinterpret_cast<uint4*>(a.bounds + (pair * a.n_blocks + blk0) * 2 * kD) + lane;
+  uint32_t w[kRows];
+  uint16_t nr[2][kGrouped ? 2 : 1];
+  // a row seen twice changes no minimum: rows past the block's last one are the last one
+  auto load_words = [&](int blk) {
+    const int last = min(TQ_BLOCK - 1, n_rows - 1 - blk * TQ_BLOCK);
+    const uint32_t* p = words + blk * TQ_BLOCK * kWords;
+    if (last == TQ_BLOCK - 1 && kGroups * kRows == TQ_BLOCK) {
 #pragma unroll
-    for (int u = 0; u < kR; ++u) {
-      const int r = min(first + g + kGroups * (kR * (it % kSteps) + u), last);
-      w[u] = __ldg(words + r * kWords);
-      nr[u] = __ldg(norms + r * n_norms);
+      for (int u = 0; u < kRows; ++u) w[u] = __ldg(p + (g + kGroups * u) * kWords);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) w[u] = __ldg(p + min(g + kGroups * u, last) * kWords);
     }
   };
-  load(0);
+  auto load_norms = [&](int blk) {
+    const int last = min(TQ_BLOCK - 1, n_rows - 1 - blk * TQ_BLOCK);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint16_t* n = norms + (blk * TQ_BLOCK + min(lane + 32 * i, last)) * n_norms;
+#pragma unroll
+      for (int j = 0; j < (kGrouped ? 2 : 1); ++j) nr[i][j] = __ldg(n + j);
+    }
+  };
+  load_norms(0);
+  load_words(0);
 #pragma unroll 1
   for (int blk = 0; blk < blocks; ++blk) {
-    float lo[2 * NP], hi[2 * NP];
+    __syncwarp();   // the last block's pools and result have been read
 #pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) { lo[i] = INFINITY; hi[i] = -INFINITY; }
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      uint32_t wc[kR];
-      float f[kR];
-#pragma unroll
-      for (int u = 0; u < kR; ++u) {
-        wc[u] = w[u];
-        f[u] = __half2float(__ushort_as_half(nr[u])) * scale;
-      }
-      if (blk * kSteps + s + 1 < blocks * kSteps) load(blk * kSteps + s + 1);
-      if (!second) bounds_step<B0, kR>(wc, f, lv, lo, hi);
-      else if constexpr (kGrouped) bounds_step<B1, kR>(wc, f, lv, lo, hi);
+    for (int i = 0; i < 2; ++i) {
+      scale_levels<B0>(lv0, __half2float(__ushort_as_half(nr[i][0])) * a.scale0, &pool[0][lane + 32 * i]);
+      if constexpr (kGrouped) scale_levels<B1x>(lv1, __half2float(__ushort_as_half(nr[i][1])) * a.scale1, &pool[1][lane + 32 * i]);
     }
-    __half2 v[2 * NP];
+    __syncwarp();
+    if (blk + 1 < blocks) load_norms(blk + 1);
+    __half2 v[2 * NP];   // minima, then maxima
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      v[i] = __floats2half2_rn(lo[2 * i], lo[2 * i + 1]);
-      v[NP + i] = __floats2half2_rn(-hi[2 * i], -hi[2 * i + 1]);
+      v[i] = __half2half2(__ushort_as_half(0x7c00));
+      v[NP + i] = __half2half2(__ushort_as_half(0xfc00));
     }
+    // rows of the pools past TQ_BLOCK - 1 do not exist; those past the last row repeat it
+    auto pool_row = [&](int u) { return kGroups * kRows == TQ_BLOCK ? g + kGroups * u : min(g + kGroups * u, TQ_BLOCK - 1); };
+#pragma unroll
+    for (int u = 0; u < kRows; u += 2) {
+      const int u1 = min(u + 1, kRows - 1);
+      const int r0 = pool_row(u), r1 = pool_row(u1);
+      if (!second) bounds_rows<B0>(w[u], w[u1], &pool[0][r0], &pool[0][r1], v);
+      else if constexpr (kGrouped) bounds_rows<B1x>(w[u], w[u1], &pool[1][r0], &pool[1][r1], v);
+    }
+    if (blk + 1 < blocks) load_words(blk + 1);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) v[NP + i] = __hneg2(v[NP + i]);
     if constexpr (!kGrouped) {
-      // 4, 8 or 16 words: the lanes of a warp that share a word end with 4 of its 2 NP results each
+      // 4, 8 or 16 words: the lanes that share a word end with 4 of its 2 NP results each
       join_lanes<16, 2 * NP>(v, lane);
       if constexpr (kWords <= 8) join_lanes<8, NP>(v, lane);
       if constexpr (kWords <= 4) join_lanes<4, NP / 2>(v, lane);
       const int at = word * NP + (kWords <= 8 ? (lane >> 3 & 1) * (NP / 2) : 0) + (kWords <= 4 ? (lane >> 2 & 1) * (NP / 4) : 0);
+      __half* o = res + (lane >> 4) * kD;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) part[tid >> 5][lane >> 4][at + i] = v[i];
-    } else if (g < kGroups) {
-      const int p = second ? NP0 * kWords0 + (word - kWords0) * NP1 : word * NP0, n = second ? NP1 : NP0;
+      for (int i = 0; i < 4; ++i) {
+        const __half2 x = lane >> 4 ? __hneg2(v[i]) : v[i];
+        o[level_channel(B0, at + i, 0)] = __low2half(x);
+        o[level_channel(B0, at + i, 1)] = __high2half(x);
+      }
+    } else {
+      __half2 (*part)[2][kD / 2] = parts[warp];
+      if (lane < kGroups * kWords) {
+        const int p = second ? NP0 * kWords0 + (word - kWords0) * NP1 : word * NP0, n = second ? NP1 : NP0;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        if (i < n) {
-          part[g][0][p + i] = v[i];
-          part[g][1][p + i] = v[NP + i];
-        }
+        for (int i = 0; i < NP; ++i)
+          if (i < n) {
+            part[g][0][p + i] = v[i];
+            part[g][1][p + i] = v[NP + i];
+          }
+      }
+      __syncwarp();
+      constexpr int pairs0 = NP0 * kWords0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int p = lane + 32 * (j & 1), which = j >> 1;
+        __half2 x = part[0][which][p];
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i) x = __hmin2(x, part[i][which][p]);
+        if (which) x = __hneg2(x);
+        const bool rest = p >= pairs0;
+        const int q = rest ? p - pairs0 : p, c0 = which * kD + (rest ? 2 * pairs0 : 0);
+        res[c0 + (rest ? level_channel(B1x, q, 0) : level_channel(B0, q, 0))] = __low2half(x);
+        res[c0 + (rest ? level_channel(B1x, q, 1) : level_channel(B0, q, 1))] = __high2half(x);
       }
     }
-    __syncthreads();
-    {
-      const int p = tid & 63, which = tid >> 6;
-      __half2 x = part[0][which][p];
-#pragma unroll 4
-      for (int i = 1; i < kParts; ++i) x = __hmin2(x, part[i][which][p]);
-      if (which) x = __hneg2(x);
-      constexpr int pairs0 = NP0 * kWords0;
-      const bool rest = kGrouped && p >= pairs0;
-      const int q = rest ? p - pairs0 : p, c0 = rest ? 2 * pairs0 : 0;
-      res[which][c0 + (rest ? level_channel(kGrouped ? B1 : 4, q, 0) : level_channel(B0, q, 0))] = __low2half(x);
-      res[which][c0 + (rest ? level_channel(kGrouped ? B1 : 4, q, 1) : level_channel(B0, q, 1))] = __high2half(x);
-    }
-    __syncthreads();
-    out[blk * kD + tid] = reinterpret_cast<const __half2*>(&res[0][0])[tid];
+    __syncwarp();
+    out[blk * (2 * kD / 8)] = reinterpret_cast<const uint4*>(res)[lane];
   }
 }
 
@@ -456,19 +516,20 @@ tq_status launch_block_bounds(const tq_quantizer* q, const tq_kv_cache* c, void*
   // the blocks that n_tokens tokens can touch, wherever they begin
   const int64_t span = (static_cast<int64_t>(n_tokens) + TQ_BLOCK - 2) / TQ_BLOCK + 1;
   const int64_t most = span < a.n_blocks ? span : a.n_blocks;
-  // up to 8 blocks a block of threads, but several rounds over the SMs so that the last one is short
+  // up to 8 blocks a warp, but several rounds over the SMs so that the last one is short
   const int64_t all = most * c->n_kv_heads * c->batch;
-  a.per_cta = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, all / (8 * 6 * std::max(1, sm_count(q->device))))));
-  const dim3 grid(static_cast<unsigned>((most + a.per_cta - 1) / a.per_cta), c->n_kv_heads, c->batch);
+  a.per_warp = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, all / (2 * 32 * std::max(1, sm_count(q->device))))));
+  const int64_t per_cta = static_cast<int64_t>(a.per_warp) * kBW;
+  const dim3 grid(static_cast<unsigned>((most + per_cta - 1) / per_cta), c->n_kv_heads, c->batch);
   const int bits = q->mode == TQ_MODE_PROD ? q->bits - 1 : q->bits;
   switch (q->mode == TQ_MODE_GROUPED ? 4 + bits : bits) {
-    case 1: k_block_bounds<1, 0><<<grid, kBT, 0, st>>>(a); break;
-    case 2: k_block_bounds<2, 0><<<grid, kBT, 0, st>>>(a); break;
-    case 3: k_block_bounds<3, 0><<<grid, kBT, 0, st>>>(a); break;
-    case 4: k_block_bounds<4, 0><<<grid, kBT, 0, st>>>(a); break;
-    case 5: k_block_bounds<2, 1><<<grid, kBT, 0, st>>>(a); break;
-    case 6: k_block_bounds<3, 2><<<grid, kBT, 0, st>>>(a); break;
-    default: k_block_bounds<4, 3><<<grid, kBT, 0, st>>>(a); break;
+    case 1: k_block_bounds<1, 0><<<grid, 32 * kBW, 0, st>>>(a); break;
+    case 2: k_block_bounds<2, 0><<<grid, 32 * kBW, 0, st>>>(a); break;
+    case 3: k_block_bounds<3, 0><<<grid, 32 * kBW, 0, st>>>(a); break;
+    case 4: k_block_bounds<4, 0><<<grid, 32 * kBW, 0, st>>>(a); break;
+    case 5: k_block_bounds<2, 1><<<grid, 32 * kBW, 0, st>>>(a); break;
+    case 6: k_block_bounds<3, 2><<<grid, 32 * kBW, 0, st>>>(a); break;
+    default: k_block_bounds<4, 3><<<grid, 32 * kBW, 0, st>>>(a); break;
   }
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
 }

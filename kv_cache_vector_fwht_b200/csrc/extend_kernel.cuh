@@ -173,7 +173,7 @@ __device__ __forceinline__ int operand_position(int bits, int c) {
   }
   if (bits == 2) {
     const int i = c & 15;
-    return (c & ~15) + (i & 1 ? 8 + (i >> 1) : i >> 1);
+    return (c & ~15) + 4 * (i & 3) + (i >> 2);
   }
   return c;
 }

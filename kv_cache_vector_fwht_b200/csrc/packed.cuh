@@ -20,7 +20,7 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 }
 
 // Byte pools of a codebook (DevTables::lv_lo, lv_hi): the levels over DevTables::lv_scale in fp16
-// (4-bit codes: the positive half; 1-bit: lo[0] is the positive level twice).
+// (4-bit codes: the positive half; 2-bit: lo is the four levels; 1-bit: lo[0] is the positive level twice).
 struct Levels {
   uint32_t lo[2], hi[2];
 };
@@ -34,7 +34,7 @@ __host__ __device__ constexpr int level_pairs(int bits) { return bits == 1 ? 16 
 
 // Element e (0, 1) of pair i of a word: which of the word's codes it is.
 __host__ __device__ constexpr int level_code(int bits, int i, int e) {
-  return bits == 1 ? i + 16 * e : bits == 2 ? (i < 4 ? 2 * (2 * i + e) : 2 * (2 * (i - 4) + e) + 1) : 2 * i + e;
+  return bits == 1 ? i + 16 * e : bits == 2 ? 4 * (2 * (i & 1) + e) + i / 2 : 2 * i + e;
 }
 // Element e of pair p of a run of words: its channel in the run.
 __host__ __device__ constexpr int level_channel(int bits, int p, int e) {
@@ -55,13 +55,13 @@ __device__ __forceinline__ void unpack_levels(uint32_t w, const Levels& t, uint3
 #pragma unroll
     for (int i = 0; i < 16; ++i) out[i] = sign_level(inv, i, t.lo[0]);
   } else if constexpr (BITS == 2) {
-    const uint32_t c[2] = {w & 0x33333333u, (w >> 2) & 0x33333333u};
+    // code c is bytes 2c and 2c + 1 of the four levels: a byte of selectors is 0x22 c + 0x10
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t sel = i & 1 ? c[i >> 1] >> 16 : c[i >> 1];
-      const uint32_t l = prmt(t.lo[0], 0, sel), h = prmt(t.hi[0], 0, sel);
-      out[2 * i] = prmt(l, h, 0x5140);
-      out[2 * i + 1] = prmt(l, h, 0x7362);
+      const uint32_t c = (w >> (2 * i)) & 0x03030303u;
+      const uint32_t sel = c * 0x22u + 0x10101010u;
+      out[2 * i] = prmt(t.lo[0], t.lo[1], sel);
+      out[2 * i + 1] = prmt(t.lo[0], t.lo[1], sel >> 16);
     }
   } else if constexpr (BITS == 3) {
     const uint32_t c = w & 0x77777777u;   // a selector with bit 3 set would spread the byte's sign

@@ -195,6 +195,8 @@ float level_bytes(const double* cent, int bits, uint32_t (&lo)[2], uint32_t (&hi
   if (bits == 1) {
     const uint32_t h = float_to_half_bits_rn(cent[1] * best);
     lo[0] = h | (h << 16);
+  } else if (bits == 2) {
+    for (int k = 0; k < n; ++k) lo[k >> 1] |= static_cast<uint32_t>(float_to_half_bits_rn(cent[k] * best)) << (16 * (k & 1));
   } else {
     const int first = bits == 4 ? half : 0, count = bits == 4 ? half : n;
     for (int k = 0; k < count; ++k) {

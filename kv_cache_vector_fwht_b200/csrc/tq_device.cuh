@@ -81,15 +81,10 @@ __device__ __forceinline__ void fwht_reg(float* v) {
   }
 }
 
-// Three-way minimum and maximum (sm_100: one instruction each).
+// Three-way maximum (sm_100: one instruction).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float y;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 

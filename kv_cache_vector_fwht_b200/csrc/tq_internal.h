@@ -43,7 +43,8 @@ struct DevTables {
   // the 32 lanes of a round write 32 different shared-memory banks.
   uint8_t gsched[32][4];
   // fp16 levels of the codebooks as byte pools for permute lookups (packed.cuh): the level set
-  // (4-bit codes: its positive half; 1-bit: the positive level twice in lv_lo[0]) divided by
+  // (4-bit codes: its positive half; 2-bit: the levels themselves in lv_lo, 1-bit: the positive one
+  // twice in lv_lo[0]) divided by
   // lv_scale, a factor chosen so that every level is an fp16 number to 2^-13 or better.
   uint32_t lv_lo[2][2], lv_hi[2][2];
   float lv_scale[2];
