@@ -199,11 +199,12 @@ def _dtype_code(t) -> int:
     return 99
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device: int | None = None) -> int | None:
+    """Raw handle of `stream`; None: the current one (of `device`, the current one, if known)."""
     import torch
     if stream is None:
         try:   # raw handle of the current stream without building a Stream object
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
         except AttributeError:
             return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
@@ -484,13 +485,15 @@ def _require(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _on_current_device(where: str, *tensors) -> None:
-    """Launches go to the current device; a tensor of another one is refused."""
+def _on_current_device(where: str, *tensors) -> int:
+    """The current device, which launches go to; a tensor of another one is refused."""
     import torch
-    cur = torch.cuda.current_device()
+    # a tensor on a GPU has initialised CUDA: the plain getter is enough
+    cur = torch._C._cuda_getDevice() if tensors[0].is_cuda else torch.cuda.current_device()
     for t in tensors:
         if t.get_device() != cur:   # -1: not on a GPU
             raise ValueError(f"{where}: tensors must be on the current CUDA device ({cur}), got {t.device}")
+    return cur
 
 
 def _heads(x) -> Heads:
@@ -532,7 +535,7 @@ def tq_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weigh
         raise ValueError("tq_norm_rope: positions are int32 (n_axes, batch, n_tokens), contiguous")
     if not (inv_freq.dim() == 1 and inv_freq.dtype == torch.float32 and inv_freq.is_contiguous()):
         raise ValueError("tq_norm_rope: inv_freq is a contiguous fp32 vector")
-    _on_current_device("tq_norm_rope", x, positions, inv_freq)
+    device = _on_current_device("tq_norm_rope", x, positions, inv_freq)
     pairs = inv_freq.shape[0]
     axes = None
     if axis_of_freq is not None:
@@ -544,7 +547,7 @@ def tq_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weigh
     if norm is None:
         norm = q_weight is not None or k_weight is not None
     st = _lib.tq_norm_rope(ctypes.byref(rope), _dtype_code(x), batch, n_tokens, D, *q_args, *k_args, norm, eps,
-                           _stream(stream))
+                           _stream(stream, device))
     if st != TQ_OK:
         _check(st, "tq_norm_rope")
 
@@ -595,12 +598,12 @@ def tq_extend_attention(q: Quantizer, cache: KVCache, query, out, workspace, cau
              f"{where}: query is (batch, n_q_heads, n_tokens, 128)")
     _require(out.shape == query.shape, f"{where}: out has query's shape")
     _require(query.stride(3) == 1 and out.stride(3) == 1, f"{where}: channels must be adjacent")
-    _on_current_device(where, query, out, workspace, cache.k_idx)
+    device = _on_current_device(where, query, out, workspace, cache.k_idx)
     _check(_lib.tq_extend_attention(q.handle, ctypes.byref(cache.desc), _heads(query),
                                     _dtype_code(query), query.shape[1], query.shape[2], int(causal),
                                     _head_map(head_map, query.shape[1], where), sm_scale, _heads(out),
                                     _dtype_code(out), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)), where)
+                                    workspace.numel() * workspace.element_size(), _stream(stream, device)), where)
 
 
 def alloc_block_bounds(cache: KVCache, device="cuda"):
@@ -619,9 +622,9 @@ def _check_bounds(cache: KVCache, bounds, where: str) -> None:
 def tq_block_bounds(q: Quantizer, cache: KVCache, bounds, n_tokens: int, stream=None) -> None:
     """Recompute the bounds of the blocks that hold the last n_tokens tokens of every sequence."""
     _check_bounds(cache, bounds, "tq_block_bounds")
-    _on_current_device("tq_block_bounds", bounds, cache.k_idx)
+    device = _on_current_device("tq_block_bounds", bounds, cache.k_idx)
     _check(_lib.tq_block_bounds(q.handle, ctypes.byref(cache.desc), _ptr(bounds), n_tokens,
-                                _stream(stream)), "tq_block_bounds")
+                                _stream(stream, device)), "tq_block_bounds")
 
 
 def tq_blocks_workspace_bytes(cache: KVCache, n_q_heads: int, n_select: int) -> int:
@@ -654,12 +657,12 @@ def tq_select_blocks(q: Quantizer, cache: KVCache, bounds, query, blocks, worksp
     where = "tq_select_blocks"
     _check_bounds(cache, bounds, where)
     _check_step(cache, query, blocks, where)
-    _on_current_device(where, bounds, query, blocks, workspace, cache.k_idx)
+    device = _on_current_device(where, bounds, query, blocks, workspace, cache.k_idx)
     _check(_lib.tq_select_blocks(q.handle, ctypes.byref(cache.desc), _ptr(bounds), _ptr(query),
                                  _dtype_code(query), query.shape[1],
                                  _head_map(head_map, query.shape[1], where), blocks.shape[2], n_sink,
                                  n_recent, _ptr(blocks), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)), where)
+                                 workspace.numel() * workspace.element_size(), _stream(stream, device)), where)
 
 
 def tq_decode_attention_blocks(q: Quantizer, cache: KVCache, query, blocks, out, workspace,
@@ -669,10 +672,10 @@ def tq_decode_attention_blocks(q: Quantizer, cache: KVCache, query, blocks, out,
     where = "tq_decode_attention_blocks"
     _check_step(cache, query, blocks, where)
     _require(out.shape == query.shape and out.is_contiguous(), f"{where}: out has query's shape, contiguous")
-    _on_current_device(where, query, blocks, out, workspace, cache.k_idx)
+    device = _on_current_device(where, query, blocks, out, workspace, cache.k_idx)
     _check(_lib.tq_decode_attention_blocks(q.handle, ctypes.byref(cache.desc), _ptr(query),
                                            _dtype_code(query), query.shape[1],
                                            _head_map(head_map, query.shape[1], where), sm_scale,
                                            _ptr(blocks), blocks.shape[2], _ptr(out), _dtype_code(out),
                                            _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                           _stream(stream)), where)
+                                           _stream(stream, device)), where)

@@ -233,16 +233,20 @@ __global__ void __launch_bounds__(32 * kBW, B0 == 2 && B1 == 0 ? 8 : 5) k_block_
 // there and the sums are off by 2^-53, so the choice of blocks does not hang on the order of
 // a sum, at 1/2 of the fp32 rate for a few million products. A warp holds 4 channels per lane
 // of kHG rotated heads in registers and walks its blocks; the bounds are read once, 16 bytes
-// a lane. The last block of threads of a (sequence, KV head) to finish picks the blocks:
-// the n-th largest key is found by histograms of 1024 equal key ranges, each pass inside the
-// range that holds it (1-3 passes for keys that differ), and the chosen blocks are written in
-// ascending order by one prefix sum.
+// a lane; a block of threads walks as many 64-block chunks as leave one round over the SMs, because
+// the heads' rotation and the joining cost as much as a chunk. The last block of threads of a
+// (sequence, KV head) to finish picks the blocks: the n-th largest key is found by a histogram
+// of 1024 equal key ranges, then by ranking the keys of the range that holds it, once they are a warp's
+// worth (further histograms inside it until then), and the chosen blocks are written in
+// ascending order by ballots. Latency bound: 2048 blocks
+// for each of 8 KV heads of 8 heads (8 MB of bounds) take 18 us: rotation and loads, two chunks in fp64 at about 3 us
+// each, the joining fence, 2 us of picking.
 constexpr int kST = 256, kSW = kST / 32;
 constexpr int kHG = 4;       // heads scored at a time
 constexpr int kHS = 16;      // rotated heads held in shared memory
 constexpr int kBPW = 8;      // blocks a warp scores
 constexpr int kBins = 1024;
-constexpr int kNearKeys = kHS * kD;   // keys that fit the rotated heads' shared memory (2048 blocks: 131072 tokens)
+constexpr int kHeldKeys = 8;   // keys a picking thread holds in registers (2048 blocks: 131072 tokens)
 constexpr unsigned long long kAlways = ~0ull;
 
 struct SelectArgs {
@@ -260,8 +264,8 @@ struct SelectArgs {
 
 __device__ __forceinline__ double shfl_xor_d(double v, int m) { return __shfl_xor_sync(kFull, v, m); }
 
-// Rotated query row (unnormalised, fp64): lane l holds coordinates 4l .. 4l + 3.
-__device__ __forceinline__ void rotate_row_f64(const SelectArgs& a, int64_t row, int lane, double (&v)[4]) {
+// A query row with the rotation's signs: lane l holds coordinates 4l .. 4l + 3.
+__device__ __forceinline__ void load_row_f64(const SelectArgs& a, int64_t row, int lane, double (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int j = 4 * lane + i;
@@ -269,9 +273,13 @@ __device__ __forceinline__ void rotate_row_f64(const SelectArgs& a, int64_t row,
     const float x = load_element(a.q, a.q_dtype, row * kD + c);
     v[i] = (a.tab->sign_bits[j >> 5] >> (j & 31)) & 1u ? -static_cast<double>(x) : static_cast<double>(x);
   }
+}
+
+// Its Hadamard transform (unnormalised).
+__device__ __forceinline__ void rotate_row_f64(bool grouped, int lane, double (&v)[4]) {
   double t0 = v[0] + v[1], t1 = v[0] - v[1], t2 = v[2] + v[3], t3 = v[2] - v[3];
   v[0] = t0 + t2; v[2] = t0 - t2; v[1] = t1 + t3; v[3] = t1 - t3;
-  const int top = a.grouped ? 4 : 16;   // grouped: 32-point blocks
+  const int top = grouped ? 4 : 16;   // grouped: 32-point blocks
   for (int m = 1; m <= top; m <<= 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -286,113 +294,142 @@ __device__ __forceinline__ unsigned long long order_key(double s) {
   return b < 0 ? ~static_cast<unsigned long long>(b) : static_cast<unsigned long long>(b) | (1ull << 63);
 }
 
-// Inclusive prefix sum over the block's threads (two-level, kSW warps).
-__device__ __forceinline__ int block_scan(int v, int* warp_sums) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  for (int m = 1; m < 32; m <<= 1) {
-    const int o = __shfl_up_sync(kFull, v, m);
-    if (lane >= m) v += o;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[w] = v;
-  __syncthreads();
-  for (int i = 0; i < w; ++i) v += warp_sums[i];
-  return v;
-}
-
-// The blocks of one (sequence, KV head), by all threads of the block.
-__device__ void pick_blocks(const SelectArgs& a, int pair, int nb, unsigned long long* near) {
-  __shared__ unsigned hist[kBins];
-  __shared__ int sums[kSW];
-  __shared__ unsigned long long s_lo, s_hi;
-  __shared__ int s_bin, s_need;
-  const int tid = threadIdx.x;
+// The blocks of one (sequence, KV head), by all threads of the block. Warp w looks at the keys
+// [w span, (w + 1) span), lane by lane; keys are never 0, which stands for an absent one.
+__device__ void pick_blocks(const SelectArgs& a, int pair, int nb) {
+  __shared__ __align__(16) uint4 hist4[kBins / 4];
+  __shared__ unsigned sums[kSW][2];
+  __shared__ int scans[kSW];
+  __shared__ unsigned long long few[32];
+  __shared__ int s_bin, s_need, s_count, s_few;
+  unsigned* hist = reinterpret_cast<unsigned*>(hist4);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const unsigned below = (1u << lane) - 1;
   int32_t* ids = a.ids + static_cast<int64_t>(pair) * a.n_select;
   if (nb <= a.n_select) {
     for (int i = tid; i < a.n_select; i += kST) ids[i] = i < nb ? i : -1;
     return;
   }
-  // the keys are read several times: from shared memory where they fit
   const unsigned long long* keys = a.keys + static_cast<int64_t>(pair) * a.n_blocks;
-  if (nb <= kNearKeys) {
-    for (int i = tid; i < nb; i += kST) near[i] = __ldcg(keys + i);
-    __syncthreads();
-    keys = near;
+  const int span = ((nb + kSW - 1) / kSW + 31) & ~31;
+  const bool held = span <= 32 * kHeldKeys;
+  unsigned long long mine[kHeldKeys];
+  if (held) {
+#pragma unroll
+    for (int j = 0; j < kHeldKeys; ++j) {
+      const int i = w * span + 32 * j + lane;
+      mine[j] = 32 * j < span && i < nb ? __ldcg(keys + i) : 0;
+    }
   }
+  auto each = [&](auto f) {   // f(block, key), the warp's lanes together
+    if (held) {
+#pragma unroll
+      for (int j = 0; j < kHeldKeys; ++j)
+        if (32 * j < span) f(w * span + 32 * j + lane, mine[j]);
+    } else {
+      for (int j = 0; j < span; j += 32) {
+        const int i = w * span + j + lane;
+        f(i, i < nb ? __ldcg(keys + i) : 0ull);
+      }
+    }
+  };
   int need = a.n_select - a.n_sink - a.n_recent;   // nb > n_select: the two ranges do not meet
   unsigned long long T = kAlways;                  // the smallest key chosen ...
   int ties = 0;                                    // ... and how many of its equals
   if (need > 0) {
-    unsigned long long lo = ~0ull, hi = 0;
-    for (int i = tid; i < nb; i += kST) {
-      const unsigned long long k = keys[i];
-      if (k != kAlways) { lo = min(lo, k); hi = max(hi, k); }
-    }
-    if (tid == 0) { s_lo = ~0ull; s_hi = 0; }
+    unsigned lo32 = ~0u, hi32 = 0;   // of the keys' high words
+    each([&](int, unsigned long long k) {
+      if (k != 0 && k != kAlways) {
+        lo32 = min(lo32, static_cast<unsigned>(k >> 32));
+        hi32 = max(hi32, static_cast<unsigned>(k >> 32));
+      }
+    });
+    lo32 = __reduce_min_sync(kFull, lo32);
+    hi32 = __reduce_max_sync(kFull, hi32);
+    if (lane == 0) { sums[w][0] = lo32; sums[w][1] = hi32; }
+    hist4[tid] = make_uint4(0, 0, 0, 0);
+    static_assert(kBins == 4 * kST, "four bins a thread");
     __syncthreads();
-    for (int m = 16; m >= 1; m >>= 1) {
-      lo = min(lo, __shfl_xor_sync(kFull, lo, m));
-      hi = max(hi, __shfl_xor_sync(kFull, hi, m));
-    }
-    if ((tid & 31) == 0) { atomicMin(&s_lo, lo); atomicMax(&s_hi, hi); }
-    __syncthreads();
-    lo = s_lo; hi = s_hi;
+    for (int i = 0; i < kSW; ++i) { lo32 = min(lo32, sums[i][0]); hi32 = max(hi32, sums[i][1]); }
+    unsigned long long lo = static_cast<unsigned long long>(lo32) << 32, hi = static_cast<unsigned long long>(hi32) << 32 | 0xffffffffull;
     while (true) {   // at most 7 turns: each leaves at most a 2^-9 of the key range
       const int width = 64 - __clzll(static_cast<long long>(hi - lo));
       const int s = max(0, width - 10);
-      for (int i = tid; i < kBins; i += kST) hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < nb; i += kST) {
-        const unsigned long long k = keys[i];
-        if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> s], 1u);
-      }
+      each([&](int, unsigned long long k) {
+        if (k >= lo && k <= hi && k != kAlways) atomicAdd(&hist[(k - lo) >> s], 1u);
+      });
       __syncthreads();
       // thread t sums the bins [1024 - 4t - 4, 1024 - 4t): a scan from the highest bin down
-      constexpr int per = kBins / kST;
-      int mine = 0;
-      for (int i = 0; i < per; ++i) mine += hist[kBins - 1 - (per * tid + i)];
-      const int upto = block_scan(mine, sums);
-      if (upto >= need && upto - mine < need) {
-        int above = upto - mine, bin = kBins - 1 - per * tid;
-        while (above + static_cast<int>(hist[bin]) < need) above += hist[bin--];
-        s_bin = bin;
+      const int top = kBins - 1 - 4 * tid;
+      const uint4 h4 = hist4[kST - 1 - tid];
+      hist4[kST - 1 - tid] = make_uint4(0, 0, 0, 0);   // for the next turn
+      const int h[4] = {static_cast<int>(h4.w), static_cast<int>(h4.z), static_cast<int>(h4.y), static_cast<int>(h4.x)};
+      const int sum = h[0] + h[1] + h[2] + h[3];
+      int upto = sum;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(kFull, upto, m);
+        if (lane >= m) upto += o;
+      }
+      if (lane == 31) scans[w] = upto;
+      if (tid == 0) s_few = 0;
+      __syncthreads();
+      for (int i = 0; i < kSW; ++i) upto += i < w ? scans[i] : 0;
+      if (upto >= need && upto - sum < need) {
+        int above = upto - sum, i = 0;
+        while (above + h[i] < need) above += h[i++];
+        s_bin = top - i;
         s_need = need - above;
+        s_count = h[i];
       }
       __syncthreads();
-      const int bin = s_bin;
       need = s_need;
-      const int count = hist[bin];
-      const unsigned long long first = lo + (static_cast<unsigned long long>(bin) << s);
-      const unsigned long long last = first + ((1ull << s) - 1);
-      __syncthreads();
-      lo = first;
-      hi = min(hi, last);
+      const int count = s_count;
+      lo += static_cast<unsigned long long>(s_bin) << s;
+      hi = lo + min(hi - lo, (1ull << s) - 1);   // the sum may not pass 2^64: a NaN's key is near it
       if (s == 0 || count == need) {
         T = lo;
         ties = s == 0 ? need : nb;   // count == need: everything from lo on, its equals too
         break;
       }
+      if (count <= 32) {   // rank them
+        each([&](int, unsigned long long k) {
+          if (k >= lo && k <= hi && k != kAlways) few[atomicAdd(&s_few, 1)] = k;
+        });
+        __syncthreads();
+        const unsigned long long x = lane < count ? few[lane] : 0;
+        int greater = 0, as_great = 0;
+        for (int i = 0; i < count; ++i) {
+          greater += few[i] > x;
+          as_great += few[i] >= x;
+        }
+        const int src = __ffs(__ballot_sync(kFull, greater < need && need <= as_great)) - 1;
+        T = __shfl_sync(kFull, x, src);
+        ties = need - __shfl_sync(kFull, greater, src);
+        break;
+      }
     }
+    __syncthreads();   // sums is free
   }
-  // thread t decides the blocks [t per, (t + 1) per)
-  const int per = (nb + kST - 1) / kST;
-  const int i0 = min(nb, tid * per), i1 = min(nb, i0 + per);
-  int eq = 0, more = 0;
-  for (int i = i0; i < i1; ++i) {
-    const unsigned long long k = keys[i];
-    eq += k == T && T != kAlways;
-    more += k > T || k == kAlways;
-  }
-  const int eq_before = block_scan(eq, sums) - eq;
-  const int eq_taken = max(0, min(eq, ties - eq_before));
-  const int end = block_scan(more + eq_taken, sums);
-  int at = end - more - eq_taken, e = 0;
-  for (int i = i0; i < i1; ++i) {
-    const unsigned long long k = keys[i];
-    bool take = k > T || k == kAlways;
-    if (!take && k == T) take = e++ < eq_taken;
-    if (take) ids[at++] = i;
-  }
+  int more = 0, eq = 0;
+  each([&](int, unsigned long long k) {
+    more += __popc(__ballot_sync(kFull, k > T || k == kAlways));
+    eq += __popc(__ballot_sync(kFull, k == T && k != kAlways));
+  });
+  if (lane == 0) { sums[w][0] = more; sums[w][1] = eq; }
+  __syncthreads();
+  int at = 0, seen = 0;   // blocks chosen and equals met before this warp's
+  for (int i = 0; i < w; ++i) { at += sums[i][0]; seen += sums[i][1]; }
+  at += min(ties, seen);
+  each([&](int i, unsigned long long k) {
+    const bool is_eq = k == T && k != kAlways;
+    const unsigned e = __ballot_sync(kFull, is_eq);
+    const bool take = k > T || k == kAlways || (is_eq && seen + __popc(e & below) < ties);
+    const unsigned t = __ballot_sync(kFull, take);
+    if (take) ids[at + __popc(t & below)] = i;
+    at += __popc(t);
+    seen += __popc(e);
+  });
 }
 
 __global__ void __launch_bounds__(kST, 1) k_select_blocks(const __grid_constant__ SelectArgs a) {
@@ -400,35 +437,46 @@ __global__ void __launch_bounds__(kST, 1) k_select_blocks(const __grid_constant_
   __shared__ bool last;
   const int b = blockIdx.z, kv = blockIdx.y, pair = b * a.n_kv_heads + kv;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int h0 = a.heads.start[kv], nh = a.heads.start[kv + 1] - h0;
+  // a row of the KV head's query heads; heads are scored four at a time: an absent one repeats the last
+  auto head_row = [&](int r) { return static_cast<int64_t>(b) * a.n_q_heads + a.heads.head[h0 + r]; };
+  double first[4];   // this warp's first row, loaded beside the length
+  if (nh) load_row_f64(a, head_row(min(w, min(kHS, nh) - 1)), lane, first);
   const int len = max(0, min(a.len[b], a.capacity));
   const int nb = (len + TQ_BLOCK - 1) / TQ_BLOCK;
-  const int h0 = a.heads.start[kv], nh = a.heads.start[kv + 1] - h0;
-  const int blk0 = (blockIdx.x * kSW + w) * kBPW;
-  // the bounds are on their way while the heads are rotated; blocks past the last repeat it
-  uint2 lo2[kBPW], hi2[kBPW];
-  if (nb > a.n_select && static_cast<int>(blockIdx.x) * kSW * kBPW < nb) {
-#pragma unroll
-    for (int i = 0; i < kBPW; ++i) {
-      const uint2* p = reinterpret_cast<const uint2*>(
-          a.bounds + (static_cast<int64_t>(pair) * a.n_blocks + min(blk0 + i, nb - 1)) * 2 * kD) + lane;
-      lo2[i] = __ldg(p);
-      hi2[i] = __ldg(p + 32);
-    }
-  }
   if (nb > a.n_select) {   // else every block is chosen and no score is needed
-    double best = nh ? -INFINITY : 0.0;   // of block blk0 + lane / 4
-    if (static_cast<int>(blockIdx.x) * kSW * kBPW < nb) {
+    int rotated = -1;      // first of the rotated heads in qs
+    for (int chunk = blockIdx.x; chunk * kSW * kBPW < nb; chunk += gridDim.x) {
+      const int blk0 = (chunk * kSW + w) * kBPW;
+      // the bounds are on their way while the heads are rotated; blocks past the last repeat it
+      uint2 lo2[kBPW], hi2[kBPW];
+#pragma unroll
+      for (int i = 0; i < kBPW; ++i) {
+        const uint2* p = reinterpret_cast<const uint2*>(
+            a.bounds + (static_cast<int64_t>(pair) * a.n_blocks + min(blk0 + i, nb - 1)) * 2 * kD) + lane;
+        lo2[i] = __ldg(p);
+        hi2[i] = __ldg(p + 32);
+      }
+      double best = nh ? -INFINITY : 0.0;   // of block blk0 + lane / 4
       for (int r0 = 0; r0 < nh; r0 += kHS) {
         const int nr = min(kHS, nh - r0);
-        __syncthreads();
-        for (int r = w; r < (nr + kHG - 1) / kHG * kHG; r += kSW) {
-          double v[4] = {0.0, 0.0, 0.0, 0.0};
-          // heads are scored four at a time: an absent one repeats the last
-          rotate_row_f64(a, static_cast<int64_t>(b) * a.n_q_heads + a.heads.head[h0 + r0 + min(r, nr - 1)], lane, v);
+        if (rotated != r0) {
+          __syncthreads();
+          for (int r = w; r < (nr + kHG - 1) / kHG * kHG; r += kSW) {
+            double v[4];
+            if (rotated < 0 && r == w) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) qs[r][4 * lane + i] = v[i];
+              for (int i = 0; i < 4; ++i) v[i] = first[i];
+            } else {
+              load_row_f64(a, head_row(r0 + min(r, nr - 1)), lane, v);
+            }
+            rotate_row_f64(a.grouped, lane, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qs[r][4 * lane + i] = v[i];
+          }
+          __syncthreads();
+          rotated = r0;
         }
-        __syncthreads();
         for (int g = 0; g < nr; g += kHG) {
           double q[kHG][4];
 #pragma unroll
@@ -472,11 +520,11 @@ __global__ void __launch_bounds__(kST, 1) k_select_blocks(const __grid_constant_
           if (isnan(x) || x > best) best = x;
         }
       }
+      const int blk = blk0 + (lane >> 2);
+      if ((lane & 3) == 0 && blk < nb)
+        a.keys[static_cast<int64_t>(pair) * a.n_blocks + blk] =
+            blk < a.n_sink || blk >= nb - a.n_recent ? kAlways : order_key(best);
     }
-    const int blk = blk0 + (lane >> 2);
-    if ((lane & 3) == 0 && blk < nb)
-      a.keys[static_cast<int64_t>(pair) * a.n_blocks + blk] =
-          blk < a.n_sink || blk >= nb - a.n_recent ? kAlways : order_key(best);
   }
   // the last block of threads of this (sequence, KV head) picks
   __syncthreads();
@@ -488,7 +536,7 @@ __global__ void __launch_bounds__(kST, 1) k_select_blocks(const __grid_constant_
   __syncthreads();
   if (last) {
     __threadfence();
-    pick_blocks(a, pair, nb, reinterpret_cast<unsigned long long*>(&qs[0][0]));
+    pick_blocks(a, pair, nb);
   }
 }
 
@@ -559,7 +607,9 @@ tq_status launch_select_blocks(const tq_quantizer* q, const tq_kv_cache* c, cons
   a.q_dtype = q_dtype;
   a.grouped = q->mode == TQ_MODE_GROUPED;
   fill_head_lists(n_q_heads, c->n_kv_heads, head_map, &a.heads);
-  const dim3 grid((a.n_blocks + kSW * kBPW - 1) / (kSW * kBPW), c->n_kv_heads, c->batch);
+  const int64_t chunks = (a.n_blocks + kSW * kBPW - 1) / (kSW * kBPW), pairs = static_cast<int64_t>(c->n_kv_heads) * c->batch;
+  const int64_t sms = std::max(1, sm_count(q->device)), per = (chunks * pairs + sms - 1) / sms;   // chunks of a block of threads
+  const dim3 grid(static_cast<unsigned>((chunks + per - 1) / per), c->n_kv_heads, c->batch);
   k_select_blocks<<<grid, kST, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
 }

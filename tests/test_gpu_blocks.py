@@ -139,6 +139,40 @@ def test_selection_of_many_blocks_and_uneven_heads():
     assert np.array_equal(ids.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("kind", ["nan few", "nan many", "nan all", "close", "close and far", "equal", "low and nan"])
+@pytest.mark.parametrize("select,blocks", [(3, 700), (40, 700), (300, 700), (40, 2100), (700, 2100), (9, 41)])
+def test_selection_of_crowded_scores(kind, select, blocks):
+    """Scores of which many are NaN, equal or apart by the last bits: the threshold among its like."""
+    require_cuda()
+    qo, qg = quantizers("mse", 3)
+    g = np.random.default_rng(select)
+    lengths = [64 * blocks - 9, 64 * (blocks - 30)]
+    cache = tq.KVCache(qg, 2, 2, 64 * blocks, value_bits=0, device="cuda:0")
+    cache.set_lengths(lengths)
+    bounds = make_bounds(g, 2, 2, blocks)
+    if kind.startswith("nan"):
+        share = {"nan few": 0.01, "nan many": 0.5, "nan all": 1.0}[kind]
+        bounds[g.random((2, 2, blocks)) < share, 1, 77] = np.nan
+    elif kind == "low and nan":
+        bounds = (-40000 * np.ones(bounds.shape)).astype(np.float16)
+        bounds[:, :, ::3, 0, 5] = np.nan
+    else:
+        bounds[:] = bounds[:, :, :1]
+        if kind != "equal":   # 60 scores, a multiple of 2^-10 |q_3| apart
+            bounds[:, :, :, 0, 3] = -1 - 2.0 ** -10 * (np.arange(blocks) % 60)
+            bounds[:, :, :, 1, 3] = 1 + 2.0 ** -10 * (np.arange(blocks) % 60)
+        if kind == "close and far":
+            bounds[:, :, 17, 1] = 60000.0
+            bounds[:, :, 17, 0] = -60000.0
+    query = torch.from_numpy(g.standard_normal((2, 6, 128)).astype(np.float32))
+    ids = torch.empty((2, 2, select), dtype=torch.int32, device="cuda:0")
+    ws = tq.alloc_blocks_workspace(cache, 6, select)
+    tq.tq_select_blocks(qg, cache, torch.from_numpy(bounds).cuda(), query.cuda(), ids, ws, n_sink=1, n_recent=1)
+    tq.tq_sync_status()
+    want = choice(qo, bounds.astype(np.float64), query.double().numpy(), lengths, select, 1, 1, O.default_head_map(6, 2))
+    assert np.array_equal(ids.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("mode,bits,vbits", [("prod", 4, 4), ("mse", 2, 2), ("grouped", 3, 4)])
 @pytest.mark.parametrize("group,out_dtype", [(1, F32), (7, BF16), (24, F32)])
 def test_listed_blocks(mode, bits, vbits, group, out_dtype):
