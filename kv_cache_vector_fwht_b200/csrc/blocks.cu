@@ -440,6 +440,8 @@ __global__ void __launch_bounds__(kST, 1) k_select_blocks(const __grid_constant_
   const int h0 = a.heads.start[kv], nh = a.heads.start[kv + 1] - h0;
   // a row of the KV head's query heads; heads are scored four at a time: an absent one repeats the last
   auto head_row = [&](int r) { return static_cast<int64_t>(b) * a.n_q_heads + a.heads.head[h0 + r]; };
+  wait_for_grid();
+  launch_dependents();
   double first[4];   // this warp's first row, loaded beside the length
   if (nh) load_row_f64(a, head_row(min(w, min(kHS, nh) - 1)), lane, first);
   const int len = max(0, min(a.len[b], a.capacity));
@@ -610,8 +612,7 @@ tq_status launch_select_blocks(const tq_quantizer* q, const tq_kv_cache* c, cons
   const int64_t chunks = (a.n_blocks + kSW * kBPW - 1) / (kSW * kBPW), pairs = static_cast<int64_t>(c->n_kv_heads) * c->batch;
   const int64_t sms = std::max(1, sm_count(q->device)), per = (chunks * pairs + sms - 1) / sms;   // chunks of a block of threads
   const dim3 grid(static_cast<unsigned>((chunks + per - 1) / per), c->n_kv_heads, c->batch);
-  k_select_blocks<<<grid, kST, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
+  return launch_early(k_select_blocks, grid, kST, 0, st, a) == cudaSuccess ? TQ_OK : TQ_ECUDA;
 }
 
 }  // namespace tq

@@ -120,8 +120,7 @@ tq_status launch_rows(ExtendArgs& a, int blocks, cudaStream_t st) {
   const int smem = fixed + a.stages * a.stage_bytes;
   if (cudaFuncSetAttribute(k_extend<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
     return TQ_ECUDA;
-  k_extend<N><<<blocks, block_threads(N), smem, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
+  return launch_early(k_extend<N>, dim3(blocks), block_threads(N), smem, st, a) == cudaSuccess ? TQ_OK : TQ_ECUDA;
 }
 
 }  // namespace

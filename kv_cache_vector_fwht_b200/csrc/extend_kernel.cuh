@@ -287,6 +287,34 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  if (tid == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&ms.raw_full[i], 1);
+      mbar_init(&ms.raw_empty[i], 8);
+    }
+    for (int i = 0; i < kMaxKeyBufs; ++i) {
+      mbar_init(&ms.k_full[i], 4);
+      mbar_init(&ms.k_empty[i], 1);
+    }
+    for (int i = 0; i < kMaxValueBufs; ++i) {
+      mbar_init(&ms.v_full[i], 4);
+      mbar_init(&ms.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.s_full[i], 1);
+      mbar_init(&ms.p_full[i], 4);
+      mbar_init(&ms.p_empty[i], 1);
+    }
+    mbar_init(&ms.hada, 1);
+    mbar_init(&ms.q_in, 8);
+    mbar_init(&ms.hada_full, 1);
+    mbar_init(&ms.rot, 1);
+    mbar_init(&ms.sq_in, 8);
+    mbar_init(&ms.sq_full, 1);
+    mbar_init(&ms.q_full, 8);
+    fence_mbar_init();
+  }
+
   // ---- which sequence, KV head, query rows and range of tiles
   int b, local, n_splits;
   if (a.batch <= kMaxList) {
@@ -313,7 +341,9 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
   const int head0 = a.heads.start[kv], group = a.heads.start[kv + 1] - head0;
   const int row0 = rt * N;
   const int rows = min(N, group * a.n_tokens - row0);
+  wait_for_grid();   // what precedes is done; before the tensor memory is taken, which it may still hold
   if (rows <= 0) return;
+  launch_dependents();
   const int len = max(0, min(a.len[b], a.capacity));
   const int shift = a.causal ? a.n_tokens - 1 : 0;
   auto row_limit = [&](int r) {   // positions row r of this tile attends to
@@ -421,33 +451,6 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
   if (warp == wM) {
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
-  }
-  if (tid == 0) {
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&ms.raw_full[i], 1);
-      mbar_init(&ms.raw_empty[i], 8);
-    }
-    for (int i = 0; i < kMaxKeyBufs; ++i) {
-      mbar_init(&ms.k_full[i], 4);
-      mbar_init(&ms.k_empty[i], 1);
-    }
-    for (int i = 0; i < kMaxValueBufs; ++i) {
-      mbar_init(&ms.v_full[i], 4);
-      mbar_init(&ms.v_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms.s_full[i], 1);
-      mbar_init(&ms.p_full[i], 4);
-      mbar_init(&ms.p_empty[i], 1);
-    }
-    mbar_init(&ms.hada, 1);
-    mbar_init(&ms.q_in, 8);
-    mbar_init(&ms.hada_full, 1);
-    mbar_init(&ms.rot, 1);
-    mbar_init(&ms.sq_in, 8);
-    mbar_init(&ms.sq_full, 1);
-    mbar_init(&ms.q_full, 8);
-    fence_mbar_init();
   }
   if (tid < 4) ms.poison[tid] = 0x7fffffff;
   if (tid < N) ms.limit[tid] = tid < rows ? row_limit(tid) : 0;

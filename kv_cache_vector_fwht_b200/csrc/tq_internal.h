@@ -168,4 +168,20 @@ tq_status launch_select_blocks(const tq_quantizer* q, const tq_kv_cache* c, cons
                                int n_q_heads, const int32_t* head_map, int n_select, int n_sink, int n_recent, int32_t* ids,
                                void* workspace, cudaStream_t st);
 
+// Launch that may overlap the end of the stream's previous kernel; the kernel calls wait_for_grid().
+template <typename Args>
+inline cudaError_t launch_early(void (*kernel)(Args), dim3 grid, int threads, int smem, cudaStream_t st, const Args& args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 }  // namespace tq
