@@ -113,6 +113,8 @@ __global__ void __launch_bounds__(32 * kBW, B0 == 2 && B1 == 0 ? 8 : 5) k_block_
   __shared__ __align__(16) __half2 parts[kBW][kGrouped ? kGroups : 1][2][kD / 2];   // grouped: minima and negated maxima to be joined
   __shared__ __align__(16) __half res_all[kBW][2][kD];
   const int b = blockIdx.z, kv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_for_grid();
+  launch_dependents();
   const int len = min(a.len[b], a.capacity);
   const int blk0 = max(0, len - a.n_tokens) / TQ_BLOCK + (blockIdx.x * kBW + warp) * a.per_warp;
   const int n_rows = len - blk0 * TQ_BLOCK;
@@ -572,16 +574,17 @@ tq_status launch_block_bounds(const tq_quantizer* q, const tq_kv_cache* c, void*
   const int64_t per_cta = static_cast<int64_t>(a.per_warp) * kBW;
   const dim3 grid(static_cast<unsigned>((most + per_cta - 1) / per_cta), c->n_kv_heads, c->batch);
   const int bits = q->mode == TQ_MODE_PROD ? q->bits - 1 : q->bits;
+  void (*kernel)(BoundsArgs);
   switch (q->mode == TQ_MODE_GROUPED ? 4 + bits : bits) {
-    case 1: k_block_bounds<1, 0><<<grid, 32 * kBW, 0, st>>>(a); break;
-    case 2: k_block_bounds<2, 0><<<grid, 32 * kBW, 0, st>>>(a); break;
-    case 3: k_block_bounds<3, 0><<<grid, 32 * kBW, 0, st>>>(a); break;
-    case 4: k_block_bounds<4, 0><<<grid, 32 * kBW, 0, st>>>(a); break;
-    case 5: k_block_bounds<2, 1><<<grid, 32 * kBW, 0, st>>>(a); break;
-    case 6: k_block_bounds<3, 2><<<grid, 32 * kBW, 0, st>>>(a); break;
-    default: k_block_bounds<4, 3><<<grid, 32 * kBW, 0, st>>>(a); break;
+    case 1: kernel = k_block_bounds<1, 0>; break;
+    case 2: kernel = k_block_bounds<2, 0>; break;
+    case 3: kernel = k_block_bounds<3, 0>; break;
+    case 4: kernel = k_block_bounds<4, 0>; break;
+    case 5: kernel = k_block_bounds<2, 1>; break;
+    case 6: kernel = k_block_bounds<3, 2>; break;
+    default: kernel = k_block_bounds<4, 3>; break;
   }
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
+  return launch_early(kernel, grid, 32 * kBW, 0, st, a) == cudaSuccess ? TQ_OK : TQ_ECUDA;
 }
 
 size_t select_scratch_bytes(const tq_kv_cache* c) {

@@ -126,6 +126,8 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope(const __grid_constant__ 
     b = second ? b1 : b0;
     t = second ? t1 : t0;
   };
+  wait_for_grid();
+  launch_dependents();
   R xa[kBatch], xb[kBatch];
   auto fetch = [&](int r0) {
 #pragma unroll
@@ -266,22 +268,16 @@ tq_status launch_norm_rope(const tq_rope* r, int dtype, int batch, int n_tokens,
     a.axis[i] = r->axis_of_freq && i < r->rot_dim / 2 ? r->axis_of_freq[i] : 0;
   const int64_t blocks = pairs * a.chunks;
   if (blocks > 0x7fffffff) return TQ_EUNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  void (*kernel)(RopeArgs);
   const bool il = r->interleaved != 0;
   switch (dtype) {
-    case TQ_F32:
-      il ? k_norm_rope<float, true><<<grid, block, 0, st>>>(a) : k_norm_rope<float, false><<<grid, block, 0, st>>>(a);
-      break;
-    case TQ_BF16:
-      il ? k_norm_rope<__nv_bfloat16, true><<<grid, block, 0, st>>>(a)
-         : k_norm_rope<__nv_bfloat16, false><<<grid, block, 0, st>>>(a);
-      break;
-    case TQ_F16:
-      il ? k_norm_rope<__half, true><<<grid, block, 0, st>>>(a) : k_norm_rope<__half, false><<<grid, block, 0, st>>>(a);
-      break;
+    case TQ_F32: kernel = il ? k_norm_rope<float, true> : k_norm_rope<float, false>; break;
+    case TQ_BF16: kernel = il ? k_norm_rope<__nv_bfloat16, true> : k_norm_rope<__nv_bfloat16, false>; break;
+    case TQ_F16: kernel = il ? k_norm_rope<__half, true> : k_norm_rope<__half, false>; break;
     default: return TQ_EUNSUPPORTED;
   }
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ECUDA;
+  return launch_early(kernel, grid, kThreads, 0, st, a) == cudaSuccess ? TQ_OK : TQ_ECUDA;
 }
 
 }  // namespace tq

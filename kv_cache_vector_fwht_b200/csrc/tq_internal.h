@@ -181,7 +181,8 @@ inline cudaError_t launch_early(void (*kernel)(Args), dim3 grid, int threads, in
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+  return e == cudaSuccess ? e : cudaGetLastError();   // and clear it
 }
 
 }  // namespace tq
