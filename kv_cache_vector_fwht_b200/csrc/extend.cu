@@ -17,7 +17,7 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr int kFixedTiles = 10;
 
 // Query rows of a tile: the next of the kernel's sizes. Columns of the products and of the softmax that
-// hold no row cost as much as those that do (35 rows: 123 us at 64, less at 48).
+// hold no row cost as much as those that do: a tile of tokens costs about 1.0 us at 16 rows, 1.4 at 48, 2.1 at 128.
 int tile_rows(int rows) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : rows <= 64 ? 64 : rows <= 96 ? 96 : 128;
 }
@@ -35,8 +35,8 @@ struct Plan {
 };
 
 // Splits: sequence b's items (KV head x tile of query rows) get splits[b] blocks of threads each, so
-// that no block has more than T tiles; T is chosen for the fewest rounds over the SMs times (T +
-// fixed cost). The kernel divides an item's tiles by the lengths on the device: host lengths
+// that no block has more than T tiles; for one and a few more rounds over the SMs the smallest T that
+// fits is tried, and the one of the least rounds times (T + fixed cost) taken (joining: 3 tiles). The kernel divides an item's tiles by the lengths on the device: host lengths
 // only shape the split.
 Plan plan_extend(const tq_kv_cache* c, int n_tokens, int n_select, bool listed, int sms, ExtendArgs* a) {
   Plan p;
@@ -55,23 +55,28 @@ Plan plan_extend(const tq_kv_cache* c, int n_tokens, int n_select, bool listed, 
   const bool one_by_one = c->batch <= kMaxList;
   const int64_t all = items * c->batch;
   auto splits_of = [&](int b, int T) { return ((one_by_one ? tiles_of(b) : longest) + T - 1) / T; };
+  auto blocks_of = [&](int T) {
+    if (!one_by_one) return all * splits_of(0, T);
+    int64_t n = 0;
+    for (int b = 0; b < c->batch; ++b) n += items * splits_of(b, T);
+    return n;
+  };
+  const int64_t least = (all + sms - 1) / sms;   // rounds without splits
   int best_T = longest;
-  double best = 1e300;
-  if (all <= kMaxSlots) {
-    const int most_splits = static_cast<int>(std::min<int64_t>(longest, std::max<int64_t>(4, 3 * sms / all + 1)));
-    for (int s = 1; s <= most_splits; ++s) {
-      const int T = (longest + s - 1) / s;
-      int64_t blocks = 0;
-      if (one_by_one) {
-        for (int b = 0; b < c->batch; ++b) blocks += items * splits_of(b, T);
-      } else {
-        blocks = all * splits_of(0, T);
-      }
-      if (s > 1 && blocks > kMaxSlots) break;
-      const double rounds = std::ceil(static_cast<double>(blocks) / sms);
-      const double cost = rounds * (T + kFixedTiles) + (s > 1 ? 3.0 + 0.1 * s : 0.0);
-      if (cost < best) { best = cost; best_T = T; }
+  double best = static_cast<double>(least) * (longest + kFixedTiles);
+  for (int64_t rounds = least; all <= kMaxSlots && rounds < least + 4; ++rounds) {
+    // the smallest T whose blocks of threads fit the rounds
+    const int64_t room = std::min<int64_t>(rounds * sms, kMaxSlots);
+    int T = 1;
+    for (int above = longest; T < above;) {
+      const int mid = (T + above) / 2;
+      if (blocks_of(mid) <= room) above = mid;
+      else T = mid + 1;
     }
+    if (T == longest) continue;
+    const int s = (longest + T - 1) / T;
+    const double cost = static_cast<double>(rounds) * (T + kFixedTiles) + 3.0 + 0.1 * s;
+    if (cost < best) { best = cost; best_T = T; }
   }
   // More items than SMs leave a last round that few SMs share: run whole rounds of unsplit items, and split
   // the rest over all SMs (448 items of 120 tiles: three rounds and 4 items split 37 ways, not seven
