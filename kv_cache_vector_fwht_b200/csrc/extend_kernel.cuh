@@ -247,11 +247,8 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, F f) {
   return f(v[0], __shfl_xor_sync(kFull, v[0], 1));
 }
 
-// Store channels 4 lane .. 4 lane + 3 of query row `row` (token-major, then the group's heads), times f.
-__device__ __forceinline__ void store_row(const ExtendArgs& a, int b, int head0, int group, int row, int lane, float4 v,
-                                          float f) {
-  const int t = row / group, h = a.heads.head[head0 + row - t * group];
-  const int64_t at = b * a.ob + h * a.oh + t * a.ot + 4 * lane;
+// Store four channels of a query row's output at element `at`, times f.
+__device__ __forceinline__ void store_row(const ExtendArgs& a, int64_t at, float4 v, float f) {
   v.x *= f; v.y *= f; v.z *= f; v.w *= f;
   if (a.out_dtype == TQ_F32) {
     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
@@ -927,12 +924,17 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
           }
         }
       };
-      logits(true);
-      float mx = -INFINITY;
+      // no references yet: raised without a look (streams of tiles lose by the branch, 80 to 86 us at 35 rows)
+      bool raise = kByRows && i == 0;
+      if (!raise) {
+        logits(true);
+        float mx = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NS; c += 2) mx = max3(mx, x[c], x[c + 1]);
+        for (int c = 0; c < NS; c += 2) mx = max3(mx, x[c], x[c + 1]);
+        raise = named_any(1 + s, mx > kTau);
+      }
       bool waited = i == 0;
-      if (named_any(1 + s, mx > kTau)) {
+      if (raise) {
         // raise the references to the tile's maxima
         if (!waited && ok) ok = mbar_wait_ns(&ms.p_empty[s], (i - 1) & 1, kWaitNs);
         waited = true;
@@ -1008,21 +1010,30 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     // per row: its streams' factors, the joint maximum and sum (by rows: of the row's stream alone)
     float* fac0 = scal;   // free now: two factors, maximum and sum of 128 rows
     float *fac1 = fac0 + kTile, *jm = fac0 + 2 * kTile, *jl = fac0 + 3 * kTile;
-    if (tok < NS) {
+    // and 1 / sum and the output's first element, for the rows' loops to spare the divisions
+    float* inv = kByRows ? fac0 : jl + kTile / 2;
+    int64_t* out_at = reinterpret_cast<int64_t*>(sP + 2 * p_bytes(N)) - N;   // behind the last stream's sums
+    if (tok < NS && (kByRows || s == 0)) {
+      const int r = r_first + tok, t = (row0 + r) / group;
+      if (r < rows) out_at[r] = b * a.ob + a.heads.head[head0 + row0 + r - t * group] * a.oh + t * a.ot;
       const float* w0 = reinterpret_cast<float*>(sP) + tok;
       const float* w1 = reinterpret_cast<float*>(sP + p_bytes(N)) + tok;
       const float l0 = (w0[0] + w0[NS]) + (w0[2 * NS] + w0[3 * NS]);
       const float l1 = (w1[0] + w1[NS]) + (w1[2 * NS] + w1[3 * NS]);
       if (kByRows) {
-        jm[r_first + tok] = -ref[tok];
-        jl[r_first + tok] = s ? l1 : l0;
-      } else if (s == 0) {
+        const float l = s ? l1 : l0;
+        jm[r] = -ref[tok];
+        jl[r] = l;
+        inv[r] = l == 0.f ? 0.f : 1.f / l;
+      } else {
         const float m0 = -ms.ref[0][tok], m1 = -ms.ref[1][tok], m = fmaxf(m0, m1);
         const float f0 = m0 == m ? 1.f : ex2(m0 - m), f1 = m1 == m ? 1.f : ex2(m1 - m);
         fac0[tok] = f0;
         fac1[tok] = f1;
+        const float l = l0 * f0 + l1 * f1;
         jm[tok] = m;
-        jl[tok] = l0 * f0 + l1 * f1;
+        jl[tok] = l;
+        inv[tok] = l == 0.f ? 0.f : 1.f / l;
       }
     }
     named_sync(3, 256);
@@ -1046,18 +1057,29 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       if (both && s == 1) named_sync(3, 256);
     }
     named_sync(3, 256);
-#pragma unroll 4
-    for (int r = warp - wS; r < rows; r += 8) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);   // no tiles: zeros, or an empty record
-      if (nt > 0) v = reinterpret_cast<const float4*>(sV)[r * (kD / 4) + lane];
-      if (ms.poison[lane >> 3] < ms.limit[r]) v.x = v.y = v.z = v.w = __uint_as_float(0x7fffffffu);
-      const float l = jl[r];
-      if (n_splits == 1) {
-        store_row(a, b, head0, group, row0 + r, lane, v, l == 0.f ? 0.f : 1.f / l);
-      } else {
-        float* rec = a.part + (static_cast<int64_t>(blockIdx.x) * N + r) * kPartFloats;
-        reinterpret_cast<float4*>(rec + 4)[lane] = v;
-        if (lane == 0) *reinterpret_cast<float2*>(rec) = make_float2(jm[r], l);
+    const int spoilt = ms.poison[lane >> 3];
+    constexpr int kOut = kRows % 4 == 0 ? 4 : 2;   // rows whose loads overlap
+#pragma unroll 1
+    for (int r0 = warp - wS; r0 < rows; r0 += 8 * kOut) {
+      float4 v[kOut];
+#pragma unroll
+      for (int i = 0; i < kOut; ++i) {
+        const int r = min(r0 + 8 * i, rows - 1);
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);   // no tiles: zeros, or an empty record
+        if (nt > 0) v[i] = reinterpret_cast<const float4*>(sV)[r * (kD / 4) + lane];
+        if (spoilt < ms.limit[r]) v[i].x = v[i].y = v[i].z = v[i].w = __uint_as_float(0x7fffffffu);
+      }
+#pragma unroll
+      for (int i = 0; i < kOut; ++i) {
+        const int r = r0 + 8 * i;
+        if (r >= rows) break;
+        if (n_splits == 1) {
+          store_row(a, out_at[r] + 4 * lane, v[i], inv[r]);
+        } else {
+          float* rec = a.part + (static_cast<int64_t>(blockIdx.x) * N + r) * kPartFloats;
+          reinterpret_cast<float4*>(rec + 4)[lane] = v[i];
+          if (lane == 0) *reinterpret_cast<float2*>(rec) = make_float2(jm[r], jl[r]);
+        }
       }
     }
     if (n_splits > 1) {
@@ -1119,7 +1141,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
           }
 #pragma unroll
           for (int k = 0; k < kRb; ++k)
-            if (r0 + 8 * k < rows) store_row(a, b, head0, group, row0 + r0 + 8 * k, lane, O[k], L[k] == 0.f ? 0.f : 1.f / L[k]);
+            if (r0 + 8 * k < rows) store_row(a, out_at[r0 + 8 * k] + 4 * lane, O[k], L[k] == 0.f ? 0.f : 1.f / L[k]);
         }
       }
     }
