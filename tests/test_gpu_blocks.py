@@ -239,6 +239,75 @@ def test_captured_selection_and_attention():
     assert torch.equal(ids, want[0]) and torch.equal(out, want[1])
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_between_copies_fills_and_two_streams(captured):
+    """The operators directly behind copies, fills, other kernels, each other and another stream's work, all
+    of which write what they read: every pass equals one that waits after each step."""
+    require_cuda()
+    qo, qg, oc, cache, g = make_case(25, "prod", 3, 2, [6000, 2500], 2, 6016)
+    dev = "cuda:0"
+    inputs = [torch.from_numpy(W.gaussian(g, (2, 6, 1, 128))).to(BF16).to(dev) for _ in range(3)]
+    src, q, turned, half = (torch.empty_like(inputs[0]) for _ in range(4))
+    pos, pos_src = torch.zeros((2, 1), dtype=torch.int32, device=dev), torch.tensor([[5999], [2499]], dtype=torch.int32, device=dev)
+    freq = torch.from_numpy((1e4 ** -(np.arange(64) / 64)).astype(np.float32)).to(dev)
+    bounds = tq.alloc_block_bounds(cache)
+    ids = torch.empty((2, 2, 9), dtype=torch.int32, device=dev)
+    outs = [torch.empty((2, 6, 1, 128), dtype=F32, device=dev), torch.empty((2, 6, 128), dtype=F32, device=dev),
+            torch.empty((2, 6, 1, 128), dtype=F32, device=dev)]
+    ws, ws_side = (tq.alloc_extend_workspace(cache, 6, 1) for _ in range(2))
+    ws_blocks = tq.alloc_blocks_workspace(cache, 6, 9)
+    side = torch.cuda.Stream()
+
+    def run(wait=lambda: None):
+        now = torch.cuda.current_stream()
+        pos.zero_()
+        side.wait_stream(now)
+        with torch.cuda.stream(side):
+            pos.copy_(pos_src)
+        q.copy_(src)
+        now.wait_stream(side)
+        wait()
+        tq.tq_norm_rope(q, None, turned, None, pos, freq, norm=True)
+        wait()
+        bounds.zero_()
+        wait()
+        tq.tq_block_bounds(qg, cache, bounds, 6000)
+        wait()
+        tq.tq_select_blocks(qg, cache, bounds, turned[:, :, 0], ids, ws_blocks, n_sink=1, n_recent=1)
+        wait()
+        side.wait_stream(now)
+        with torch.cuda.stream(side):
+            tq.tq_extend_attention(qg, cache, turned, outs[2], ws_side)
+        wait()
+        tq.tq_decode_attention_blocks(qg, cache, turned[:, :, 0], ids, outs[1], ws_blocks)
+        wait()
+        torch.mul(turned, 0.5, out=half)
+        wait()
+        tq.tq_extend_attention(qg, cache, half, outs[0], ws)
+        wait()
+        now.wait_stream(side)
+
+    want = []
+    for x in inputs:
+        src.copy_(x)
+        run(torch.cuda.synchronize)
+        want.append([t.clone() for t in (turned, bounds, ids, *outs)])
+    assert not torch.equal(want[0][3], want[1][3])
+    again = run
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            run()
+        again = graph.replay
+    for i in range(30):
+        src.copy_(inputs[i % 3])
+        again()
+        for got, w in zip((turned, bounds, ids, *outs), want[i % 3]):
+            assert torch.equal(got, w)
+    tq.tq_sync_status()
+
+
 @pytest.mark.parametrize("mode,bits,vbits", [("prod", 4, 4), ("mse", 3, 2), ("grouped", 2, 4)])
 def test_a_prompt_and_steps_with_all_of_them(mode, bits, vbits):
     """As a model's layer uses them: the projection's rows are normed and rotated, keys and values appended, their blocks'
