@@ -108,6 +108,7 @@ Plan plan_extend(const tq_kv_cache* c, int n_tokens, int n_select, bool listed, 
     a->uniform_splits = splits_of(0, best_T);
     blocks = all * a->uniform_splits;
   }
+  a->whole = blocks == all;
   p.blocks = blocks > 0x7fffffff ? -1 : static_cast<int>(blocks);
   return p;
 }
