@@ -535,7 +535,8 @@ def tq_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weigh
         raise ValueError("tq_norm_rope: positions are int32 (n_axes, batch, n_tokens), contiguous")
     if not (inv_freq.dim() == 1 and inv_freq.dtype == torch.float32 and inv_freq.is_contiguous()):
         raise ValueError("tq_norm_rope: inv_freq is a contiguous fp32 vector")
-    device = _on_current_device("tq_norm_rope", x, positions, inv_freq)
+    if not (dev == positions.get_device() == inv_freq.get_device() >= 0 and dev == torch._C._cuda_getDevice()):
+        _on_current_device("tq_norm_rope", x, positions, inv_freq)   # says which
     pairs = inv_freq.shape[0]
     axes = None
     if axis_of_freq is not None:
@@ -547,7 +548,7 @@ def tq_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weigh
     if norm is None:
         norm = q_weight is not None or k_weight is not None
     st = _lib.tq_norm_rope(ctypes.byref(rope), _dtype_code(x), batch, n_tokens, D, *q_args, *k_args, norm, eps,
-                           _stream(stream, device))
+                           _stream(stream, dev))
     if st != TQ_OK:
         _check(st, "tq_norm_rope")
 
