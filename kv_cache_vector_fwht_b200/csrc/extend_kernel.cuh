@@ -52,7 +52,19 @@ constexpr int kMaxList = 64;            // sequences whose block counts are list
 // At 8, a tenth of the units of a 64-row stream raised (each costs three units' time); at 14 hardly
 // any but a stream's first.
 constexpr float kTau = 14.f;
-constexpr float kNoRef = -1e30f;        // reference of a row that has seen nothing
+constexpr float kNoRef = -3e38f;        // reference of a row that has seen nothing: below every finite score
+// The query rows of a tile are rounded to fp16 at one common scale (a power of two, by the largest coordinate)
+// while their largest coordinates lie within 2^8 of each other: the smallest row's rotated coordinates are then
+// 2^-10.5 in the root mean square or more, far above fp16's 2^-14. Beyond that each row has a scale of its own and
+// its column of scores a factor, multiplied out in tensor memory by the code that raises references, which every
+// unit of such a tile then runs (a factor beside the reference, in every unit's arithmetic, cost the chunk 12 %;
+// this costs it 1.4 %).
+constexpr int kSpread = 8;
+// Logits are S sc - reference in one fused step, which leaves S sc unrounded where the reference is a rounded
+// S sc: next to a logit of 2^23 the two are up to a half apart, at 2^30 64. |S| is at most 45 (a query row) x 62 (a
+// row of levels) x 2 (prod), 2^12.5, so beyond this score factor a unit that raises rounds S sc first, and its maximum
+// has a weight of 1 whatever its size.
+constexpr float kLargeFactor = 0x1p10f;
 constexpr int kNowhere = 0x40000000;    // position of a token that does not exist
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kPartFloats = 132;        // partial record: m, l, 0, 0, o[128]
@@ -116,11 +128,12 @@ struct Misc {
   uint32_t tmem;
   int last;
   int poison[4];            // per value group: lowest position of a non-finite cached value
-  float norm2[8];           // largest finite squared norm of each softmax warp's query rows
+  int sizes[8];             // row sizes of each softmax warp: the largest << 8 | the smallest
   int pos0[16][2];          // first position of a tile's two halves, by tile mod 16
   alignas(16) int limit[128];   // per row: positions it attends to
   alignas(16) float ref[2][64];   // negated references
   alignas(16) float fac[2][64];
+  alignas(16) uint8_t size[128];  // row_size of each row
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc fits");
 
@@ -143,6 +156,31 @@ __device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+// The sizes of K query rows, four coordinates of each a lane: row i's in the lanes with lane / (32 / P) == i, P the power
+// of two from K on. A row's size is the exponent (plus 127) of the power of two that brings its largest coordinate
+// to 2 .. 4; 0 for a row that sets no scale: all zeros (or next to it), or not finite.
+template <int K>
+__device__ __forceinline__ int row_sizes(const float (&v)[K][4], int lane) {
+  constexpr int P = K <= 2 ? 2 : K <= 4 ? 4 : 8;
+  uint32_t m[P] = {};
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[i] = max(m[i], __float_as_uint(v[i][k]) & 0x7fffffffu);   // NaN is above infinity
+#pragma unroll
+  for (int h = P / 2, s = 16; h >= 1; h >>= 1, s >>= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const uint32_t mine = up ? m[i + h] : m[i], theirs = up ? m[i] : m[i + h];
+      m[i] = max(mine, __shfl_xor_sync(kFull, theirs, s));
+    }
+  }
+#pragma unroll
+  for (int s = 16 / P; s >= 1; s >>= 1) m[0] = max(m[0], __shfl_xor_sync(kFull, m[0], s));
+  const int e = static_cast<int>(m[0] >> 23);
+  return e == 0 || e == 255 ? 0 : max(67, e - 1);
 }
 // Registers a thread of this warpgroup may use from here on.
 template <int R>
@@ -417,7 +455,20 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
   const bool stash = !kKeep && a.q_dtype != TQ_F32;
   uint32_t sbits = 0;
   if (warp >= wS && warp < wM) {
-    float top2 = 0.f;
+    int small = 255, large = 0;
+    auto sized = [&](int i0, const auto& v) {   // rows from the i0-th of this warp on; those that attend to nothing set no scale
+      constexpr int K = sizeof(v) / sizeof(v[0]), lanes = K <= 2 ? 16 : K <= 4 ? 8 : 4;
+      int e = row_sizes(v, lane);
+      const int i = lane / lanes, r = (warp - wS) + 8 * (i0 + i);
+      if (i < K) {
+        if (r >= rows || (low == 0 && row_limit(r) == 0)) e = 0;
+        if (e) {
+          small = min(small, e);
+          large = max(large, e);
+        }
+        if (lane % lanes == 0) ms.size[r] = static_cast<uint8_t>(e);
+      }
+    };
     sbits = a.tab->sign_bits[lane >> 3] >> (4 * (lane & 7));
     if (!kKeep && stash) {
       constexpr int kAhead = kRows % 8 == 0 ? 8 : 6;
@@ -430,29 +481,25 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
           x[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + b * a.qb +
                                                      a.heads.head[head0 + r - t * group] * a.qh + t * a.qt) + lane);
         }
+        float v[kAhead][4];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           const int r = (warp - wS) + 8 * (i0 + i);
           *reinterpret_cast<uint2*>(sQ + (r >> 3) * 16 * kcols + (r & 7) * 16 + (lane >> 1) * 128 + (lane & 1) * 8) = x[i];
-          float v[4];
-          unpack16(x[i], v);
-          const float n2 = warp_sum(v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3]);
-          if (n2 < INFINITY) top2 = fmaxf(top2, n2);
+          unpack16(x[i], v[i]);
         }
+        sized(i0, v);
       }
     } else {
 #pragma unroll 1
       for (int i0 = 0; i0 < kRows; i0 += kBatch) {
-        load_batch(i0);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const float n2 = warp_sum(qv[i][0] * qv[i][0] + qv[i][1] * qv[i][1] + qv[i][2] * qv[i][2] + qv[i][3] * qv[i][3]);
-          if (n2 < INFINITY) top2 = fmaxf(top2, n2);
-        }
-        if (8 * (i0 + kBatch) >= rows) break;
+        if (8 * i0 < rows) load_batch(i0);
+        sized(i0, qv);
       }
     }
-    if (lane == 0) ms.norm2[warp - wS] = top2;
+    small = __reduce_min_sync(kFull, small);
+    large = __reduce_max_sync(kFull, large);
+    if (lane == 0) ms.sizes[warp - wS] = large << 8 | small;
   }
 
   if (warp == wM) {
@@ -762,16 +809,24 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     const int s = (warp - wS) >> 2, tok = (warp & 3) * 32 + lane;
     uint8_t* myP = sP + s * p_bytes(N);
     float qscale = 1.f;
+    bool apart = false;   // the rows have scales of their own: every unit takes the way of those that raise
     if (nt > 0) {  // ---- the query operand: rotated rows, and S q for prod
-      float n2 = 0.f;
+      int small = 255, large = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n2 = fmaxf(n2, ms.norm2[i]);
-      // a power of two that brings the longest row to a norm of 8 .. 16 (the other rows are shorter):
-      // half the exponent of its square, less three
-      const int e = max(-60, min(60, ((static_cast<int>(__float_as_uint(n2) >> 23) - 127) >> 1) - 3));
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      qscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      const float unit = down * (a.mode == TQ_MODE_GROUPED ? 0.17677669529663688f : 0.08838834764831845f);
+      for (int i = 0; i < 8; ++i) {
+        small = min(small, ms.sizes[i] & 255);
+        large = max(large, ms.sizes[i] >> 8);
+      }
+      apart = large - small > kSpread;
+      const int common = large ? large : 127;   // also of the rows that set no scale
+      qscale = apart ? a.scale_log2 : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(common) << 23);
+      const float unit = __uint_as_float(static_cast<uint32_t>(254 - common) << 23) *
+                         (a.mode == TQ_MODE_GROUPED ? 0.17677669529663688f : 0.08838834764831845f);
+      auto own_factor = [&](int r) {   // from the common scale to the row's own
+        const int own = ms.size[r], more = common - (own ? own : common), half = more >> 1;   // up to 186: in two steps
+        return make_float2(__uint_as_float(static_cast<uint32_t>(127 + half) << 23),
+                           __uint_as_float(static_cast<uint32_t>(127 + more - half) << 23));
+      };
       if (stash) {
         // many 16-bit rows: on the tensor cores, which read them where the operand will be; a thread then
         // holds coordinate tok of its stream's half of the rows
@@ -787,6 +842,13 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
         for (int c = s * kCols; c < min(N, (s + 1) * kCols); c += 16) {
           uint32_t x[16];
           tmem_ld16_sync(tlane + kS0 + c, x);
+          if (apart) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 f = own_factor(c + i);
+              x[i] = __float_as_uint(__uint_as_float(x[i]) * f.x * f.y);
+            }
+          }
           uint8_t* col = sQ + (c >> 3) * 16 * kcols + (k >> 3) * 128 + (k & 7) * 2;
           uint8_t* pcol = sP + (c >> 3) * 2048 + (k2 >> 3) * 128 + (k2 & 7) * 2;
 #pragma unroll
@@ -816,6 +878,14 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
               for (int n = 1; kKeep && n < kBatch; ++n) v[i][k] = i0 == n ? qv[n][k] : v[i][k];
               v[i][k] = flip_sign(v[i][k] * unit, sbits, k);
             }
+          if (apart) {
+#pragma unroll
+            for (int i = 0; i < kRot; ++i) {
+              const float2 f = own_factor(first + 8 * i);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[i][k] = v[i][k] * f.x * f.y;
+            }
+          }
           if (first < rows) {
 #pragma unroll
             for (int i = 0; i < kRot; ++i) fwht_reg<4>(v[i]);
@@ -889,6 +959,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       warp_arrive(&ms.q_full, lane);
     }
 
+    const float tau = apart ? -INFINITY : kTau;
     uint64_t sum[NS / 2];   // packed pairs of fp32 sums
 #pragma unroll
     for (int i = 0; i < NS / 2; ++i) sum[i] = 0;
@@ -905,7 +976,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       const int j = kByRows ? i : 2 * i + s;
       if (ok) ok = mbar_wait_ns(&ms.s_full[s], i & 1, kWaitNs);
       tc_fence_after();
-      const float sc = scal[(j & (a.scal_ring - 1)) * kTile + tok] * qscale;
+      float sc = scal[(j & (a.scal_ring - 1)) * kTile + tok] * qscale;
       const int pos = ms.pos0[j & 15][tok >> 6] + (tok & 63);
       const bool masked = __any_sync(kFull, pos >= lowest);
       // logits (base 2) of all rows, less their references if rel; masked ones -inf
@@ -941,7 +1012,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
         float mx = -INFINITY;
 #pragma unroll
         for (int c = 0; c < NS; c += 2) mx = max3(mx, x[c], x[c + 1]);
-        raise = named_any(1 + s, mx > kTau);
+        raise = named_any(1 + s, mx > tau);
       }
       bool waited = i == 0;
       if (raise) {
@@ -949,6 +1020,22 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
         if (!waited && ok) ok = mbar_wait_ns(&ms.p_empty[s], (i - 1) & 1, kWaitNs);
         waited = true;
         tc_fence_after();
+        // scores that x would hold wrongly are multiplied out in tensor memory first
+        if (__any_sync(kFull, apart || sc > kLargeFactor)) {
+#pragma unroll 1
+          for (int c = 0; c < NS; c += 16) {
+            uint32_t y[16];
+            tmem_ld16_sync(tS + c, y);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float f = apart ? __uint_as_float(static_cast<uint32_t>(ms.size[r_first + c + q]) << 23) : 1.f;
+              y[q] = __float_as_uint(__uint_as_float(y[q]) * (f * sc));
+            }
+            tmem_st16(tS + c, y);
+          }
+          tmem_st_wait();
+          sc = 1.f;
+        }
         float* wmax = reinterpret_cast<float*>(myP);   // free: the last product has read it
         float* fac = ms.fac[s];
         logits(false);
