@@ -344,8 +344,10 @@ tq_status tq_norm_rope(const tq_rope* rope, int dtype, int batch, int n_tokens, 
  * shorter than n_tokens) yields zeros. q and out: (batch, n_q_heads, n_tokens, d) views in
  * q_dtype / out_dtype (TQ_F32, TQ_BF16 or TQ_F16); they must not overlap. The products run
  * on 16-bit tensor-core operands with 32-bit sums: rotated queries, centroids, softmax weights
- * and dequantised values are rounded to fp16 (relative 2^-11 each), the softmax statistics
- * and outputs are held in fp32. Rotated queries are rounded next to a power of two of their own size:
+ * and dequantised values are rounded to fp16 (relative 2^-11 each; weights below 2^-14 of a row's
+ * largest lose 2^-11 of the row's sum at most, all together), the softmax statistics and outputs are
+ * held in fp32 (the tensor cores cut each product off at the last bit of its sum: n tokens' products
+ * of one sign lose less than n 2^-23 of it). Rotated queries are rounded next to a power of two of their own size:
  * a row's outputs do not depend on the rows beside it, however long, and finite rows of norms
  * up to 1e30 may be given. Non-finite cached rows reach only the query rows that attend
  * to them. n_tokens = 0 is a no-op; n_q_heads * n_tokens up to 2^30.

@@ -25,8 +25,8 @@
 //                      upper 64 rows beyond. Each has its own score and output columns, reference
 //                      maxima and sums, so one's exponentials run under the other's products.
 // Softmax in base 2 relative to a reference per row that is raised only when a score exceeds
-// it by more than 14 (one vote a unit; then the stream's outputs in tensor memory and its sums
-// are scaled), so p <= 2^14 fits fp16. Statistics and sums in fp32. Rounded to fp16 (relative 2^-11
+// it by more than 15 (one vote a unit; then the stream's outputs in tensor memory and its sums
+// are scaled), so p <= 2^15 fits fp16. Statistics and sums in fp32. Rounded to fp16 (relative 2^-11
 // each): q', Sq' and rho, p, v; the levels are scaled by a common factor that makes them fp16
 // numbers to 2^-13 or better.
 //
@@ -48,10 +48,15 @@ constexpr int kTile = 128;              // tokens of a tile
 constexpr int kMaxStages = 6;
 constexpr int kMaxKeyBufs = 4, kMaxValueBufs = 3;
 constexpr int kMaxList = 64;            // sequences whose block counts are listed one by one
-// A reference is raised when a score exceeds it by more than this (base 2): weights reach 2^14 in fp16.
-// At 8, a tenth of the units of a 64-row stream raised (each costs three units' time); at 14 hardly
-// any but a stream's first.
-constexpr float kTau = 14.f;
+// A reference is raised when a score exceeds it by more than this (base 2): weights reach 2^15 in fp16. It is
+// raised to the tile's maximum less reference_gap. At a limit of 8, a tenth of the units of a 64-row stream raised
+// (each costs three units' time); at 15 hardly any but a stream's first.
+constexpr float kTau = 15.f;
+// Weights below 2^-14 are subnormal in fp16 and off by up to 2^-25 each: next to one large weight, a context of n
+// tokens that share the rest may lose n 2^-25 of the sum. References are taken so far below the maximum that this
+// stays under 2^-11, half a step of fp16, for up to 2^24 tokens of a block's range: not at all for up to 128 tiles (a
+// gap of 8 for every length cost the chunk 17 %: references are raised more often).
+__device__ __forceinline__ float reference_gap(int tiles) { return static_cast<float>(min(10, max(0, 25 - __clz(tiles - 1)))); }
 constexpr float kNoRef = -3e38f;        // reference of a row that has seen nothing: below every finite score
 // The query rows of a tile are rounded to fp16 at one common scale (a power of two, by the largest coordinate)
 // while their largest coordinates lie within 2^8 of each other: the smallest row's rotated coordinates are then
@@ -1047,7 +1052,9 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
         named_sync(1 + s, 128);
         if (tok < NS) {
           const float old = -ref[tok];
-          const float m = fmaxf(fmaxf(old, fmaxf(wmax[tok], wmax[NS + tok])), fmaxf(wmax[2 * NS + tok], wmax[3 * NS + tok]));
+          const float top = fmaxf(fmaxf(wmax[tok], wmax[NS + tok]), fmaxf(wmax[2 * NS + tok], wmax[3 * NS + tok]));
+          const float gap = reference_gap(nt), below = top - gap;   // of scores beyond 2^24 a rounded difference
+          const float m = fmaxf(old, top - below == gap ? below : top);
           fac[tok] = old == m ? 1.f : ex2(old - m);
           ref[tok] = -m;
         }
