@@ -344,12 +344,13 @@ tq_status tq_norm_rope(const tq_rope* rope, int dtype, int batch, int n_tokens, 
  * shorter than n_tokens) yields zeros. q and out: (batch, n_q_heads, n_tokens, d) views in
  * q_dtype / out_dtype (TQ_F32, TQ_BF16 or TQ_F16); they must not overlap. The products run
  * on 16-bit tensor-core operands with 32-bit sums: rotated queries, centroids, softmax weights
- * and dequantised values are rounded to fp16 (relative 2^-11 each; weights below 2^-14 of a row's
- * largest lose 2^-11 of the row's sum at most, all together), the softmax statistics and outputs are
- * held in fp32 (the tensor cores cut each product off at the last bit of its sum: n tokens' products
- * of one sign lose less than n 2^-23 of it). Rotated queries are rounded next to a power of two of their own size:
- * a row's outputs do not depend on the rows beside it, however long, and finite rows of norms
- * up to 1e30 may be given. Non-finite cached rows reach only the query rows that attend
+ * and dequantised values are rounded to fp16, relative 2^-11 each. A query's coordinates (and a
+ * grouped key's) below 2^-14 of the largest in their row are off by 2^-25 of that; a row's outputs do not
+ * depend on the rows beside it, and finite rows of norms up to 1e30 may be given. Weights
+ * below 2^-14 of a row's largest lose 2^-11 of the row's sum at most, all together. The softmax
+ * statistics and outputs are held in fp32; the tensor cores cut each product off at the last bit
+ * of its sum, so n tokens' products of one sign lose less than n 2^-23 of it. Non-finite cached
+ * rows reach only the query rows that attend
  * to them. n_tokens = 0 is a no-op; n_q_heads * n_tokens up to 2^30.
  *
  * Workspace (this call, tq_select_blocks and tq_decode_attention_blocks): zero-filled before
@@ -369,7 +370,9 @@ tq_status tq_extend_attention(const tq_quantizer* q, const tq_kv_cache* cache, t
  * [TQ_BLOCK i, TQ_BLOCK (i + 1)). bounds_dev: fp16 (batch, n_kv_heads, n_blocks, 2, d) with
  * n_blocks = ceil(capacity / TQ_BLOCK): per block the channelwise minimum [0] and maximum [1]
  * of its dequantised keys in the quantizer's rotated coordinates (the codebook part
- * n16 c[idx] / sqrt(d); grouped: the groups' coordinates side by side, as in the idx plane). */
+ * n16 c[idx] / sqrt(d); grouped: the groups' coordinates side by side, as in the idx plane). A NaN
+ * norm in a block makes its bounds NaN (grouped: those of the norm's group), and the block is then
+ * chosen before all others that are not always chosen. */
 #define TQ_BLOCK 64
 
 /* Recompute the bounds of the blocks that hold the last n_tokens tokens of every sequence
@@ -384,7 +387,8 @@ tq_status tq_block_bounds(const tq_quantizer* q, const tq_kv_cache* cache, void*
  *   max_h sum_j max((Pi q_h)_j lo_j, (Pi q_h)_j hi_j),
  * summed in fp64 so that the choice does not depend on the order of the sums. The first n_sink and the last
  * n_recent blocks of a sequence (n_sink + n_recent <= n_select) are always chosen, then the
- * highest scores (equal scores: the lower block; NaN counts as the highest). blocks_dev: int32
+ * highest scores (equal scores: the lower block; NaN counts as the highest, and where infinite
+ * bounds meet a query the score is infinite or NaN). blocks_dev: int32
  * (batch, n_kv_heads, n_select), ascending, -1 behind the last one when a sequence has fewer
  * blocks. A KV head that no query head maps to gets its sinks and recent blocks and the
  * lowest-numbered others. */

@@ -10,7 +10,8 @@ namespace {
 
 // ------------------------------------------------------------------------------- bounds
 // min and max over a block's tokens of n16 c[idx_j] / sqrt(d), channel by channel. Rounding to fp16, the
-// type of the result, is monotone: the minimum of the rounded products is the rounded minimum. So a
+// type of the result, is monotone: the minimum of the rounded products is the rounded minimum. A NaN norm stays: it
+// makes the block's bounds NaN, which the selection puts first. So a
 // token's products with the whole codebook are made first (fp32, one rounding: 4 products of a 2-bit
 // codebook, 8 of a 3-bit one, the 8 positive ones of a 4-bit one), as byte pools like the codebook's
 // own; the token's codes then look up finished fp16 numbers, two to a register, and a value costs its
@@ -82,8 +83,8 @@ __device__ __forceinline__ void bounds_rows(uint32_t w0, uint32_t w1, const uint
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const __half2 a = *reinterpret_cast<const __half2*>(&y0[i]), b = *reinterpret_cast<const __half2*>(&y1[i]);
-    v[i] = __hmin2(__hmin2(v[i], a), b);
-    v[N / 2 + i] = __hmax2(__hmax2(v[N / 2 + i], a), b);
+    v[i] = __hmin2_nan(__hmin2_nan(v[i], a), b);
+    v[N / 2 + i] = __hmax2_nan(__hmax2_nan(v[N / 2 + i], a), b);
   }
 }
 
@@ -95,7 +96,7 @@ __device__ __forceinline__ void join_lanes(__half2* v, int lane) {
   for (int i = 0; i < N / 2; ++i) {
     const __half2 a = v[i], b = v[i + N / 2];
     const __half2 mine = up ? b : a, theirs = up ? a : b;
-    v[i] = __hmin2(mine, __shfl_xor_sync(kFull, theirs, M));
+    v[i] = __hmin2_nan(mine, __shfl_xor_sync(kFull, theirs, M));
   }
 }
 
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(32 * kBW, B0 == 2 && B1 == 0 ? 8 : 5) k_block_
         const int p = lane + 32 * (j & 1), which = j >> 1;
         __half2 x = part[0][which][p];
 #pragma unroll
-        for (int i = 1; i < kGroups; ++i) x = __hmin2(x, part[i][which][p]);
+        for (int i = 1; i < kGroups; ++i) x = __hmin2_nan(x, part[i][which][p]);
         if (which) x = __hneg2(x);
         const bool rest = p >= pairs0;
         const int q = rest ? p - pairs0 : p, c0 = which * kD + (rest ? 2 * pairs0 : 0);
