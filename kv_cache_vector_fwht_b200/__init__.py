@@ -542,7 +542,8 @@ def tq_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weigh
     if axis_of_freq is not None:
         if len(axis_of_freq) != pairs:
             raise ValueError("tq_norm_rope: one axis per frequency")
-        axes = bytes(axis_of_freq)
+        # element by element: bytes() of an array (numpy, array.array) would be its memory
+        axes = bytes(axis_of_freq) if type(axis_of_freq) in (list, tuple, bytes) else bytes(iter(axis_of_freq))
     rope = Rope(positions.data_ptr(), inv_freq.data_ptr(), axes, pshape[0] if len(pshape) == 3 else 1,
                 2 * pairs, interleaved)
     if norm is None:
