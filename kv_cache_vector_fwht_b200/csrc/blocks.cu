@@ -141,10 +141,10 @@ __global__ void __launch_bounds__(32 * kBW, B0 == 2 && B1 == 0 ? 8 : 5) k_block_
     const uint32_t* p = words + blk * TQ_BLOCK * kWords;
     if (last == TQ_BLOCK - 1 && kGroups * kRows == TQ_BLOCK) {
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) w[u] = __ldg(p + (g + kGroups * u) * kWords);
+      for (int u = 0; u < kRows; ++u) w[u] = p[(g + kGroups * u) * kWords];
     } else {
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) w[u] = __ldg(p + min(g + kGroups * u, last) * kWords);
+      for (int u = 0; u < kRows; ++u) w[u] = p[min(g + kGroups * u, last) * kWords];
     }
   };
   auto load_norms = [&](int blk) {
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(32 * kBW, B0 == 2 && B1 == 0 ? 8 : 5) k_block_
     for (int i = 0; i < 2; ++i) {
       const uint16_t* n = norms + (blk * TQ_BLOCK + min(lane + 32 * i, last)) * n_norms;
 #pragma unroll
-      for (int j = 0; j < (kGrouped ? 2 : 1); ++j) nr[i][j] = __ldg(n + j);
+      for (int j = 0; j < (kGrouped ? 2 : 1); ++j) nr[i][j] = n[j];
     }
   };
   load_norms(0);
@@ -459,8 +459,8 @@ __global__ void __launch_bounds__(kST, 1) k_select_blocks(const __grid_constant_
       for (int i = 0; i < kBPW; ++i) {
         const uint2* p = reinterpret_cast<const uint2*>(
             a.bounds + (static_cast<int64_t>(pair) * a.n_blocks + min(blk0 + i, nb - 1)) * 2 * kD) + lane;
-        lo2[i] = __ldg(p);
-        hi2[i] = __ldg(p + 32);
+        lo2[i] = p[0];
+        hi2[i] = p[32];
       }
       double best = nh ? -INFINITY : 0.0;   // of block blk0 + lane / 4
       for (int r0 = 0; r0 < nh; r0 += kHS) {

@@ -433,11 +433,14 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       }
     } else if (a.q_dtype == TQ_F32) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) load4<true>(static_cast<const float*>(a.q) + at[i], 4 * lane, qv[i]);
+      for (int i = 0; i < kBatch; ++i) {
+        const float4 x = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at[i])[lane];
+        qv[i][0] = x.x; qv[i][1] = x.y; qv[i][2] = x.z; qv[i][3] = x.w;
+      }
     } else {
       uint2 x[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) x[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at[i]) + lane);
+      for (int i = 0; i < kBatch; ++i) x[i] = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at[i])[lane];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (a.q_dtype == TQ_BF16) {
@@ -483,8 +486,8 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {   // rows past the last repeat it
           const int r = row0 + min((warp - wS) + 8 * (i0 + i), rows - 1), t = r / group;
-          x[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + b * a.qb +
-                                                     a.heads.head[head0 + r - t * group] * a.qh + t * a.qt) + lane);
+          x[i] = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + b * a.qb +
+                                               a.heads.head[head0 + r - t * group] * a.qh + t * a.qt)[lane];
         }
         float v[kAhead][4];
 #pragma unroll
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       for (int h = 0; h < 2; ++h) {
         const int i = 2 * (tile0 + j) + h;
         int blk = i;
-        if (list) blk = i < a.n_select ? __ldg(list + i) : -1;
+        if (list) blk = i < a.n_select ? list[i] : -1;
         const bool in = blk >= 0 && blk < a.n_blocks && blk * TQ_BLOCK < len;
         p[h] = in ? blk * TQ_BLOCK : kNowhere;
         n[h] = in ? min(TQ_BLOCK, (len - blk * TQ_BLOCK + 15) & ~15) : 0;   // within the capacity, a multiple of 16

@@ -83,7 +83,8 @@ __device__ __forceinline__ void fwht_reg(float* v) {
 
 // A kernel launched by launch_early (tq_internal.h) may start before the stream's previous kernel has
 // ended: it waits for that, and for its writes, before it reads or writes memory. Every block of threads
-// waits, those with nothing to do too, so that the kernel cannot end before what precedes it.
+// waits, those with nothing to do too, so that the kernel cannot end before what precedes it. Such a kernel reads
+// what others write with plain or .cg loads: __ldg is for memory that stays as it is while the kernel runs, its wait included.
 __device__ __forceinline__ void wait_for_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The next such kernel's blocks of threads may take their places as this one's leave.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
