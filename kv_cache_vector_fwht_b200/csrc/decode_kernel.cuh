@@ -743,28 +743,28 @@ __global__ void __launch_bounds__(Shape<NSET>::threads, 1) k_decode(const __grid
         if constexpr (IB % 16 == 0) {
 #pragma unroll
           for (int i = 0; i < IB / 16; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(row) + i);
+            const uint4 v = reinterpret_cast<const uint4*>(row)[i];
             iw[4 * i] = v.x; iw[4 * i + 1] = v.y; iw[4 * i + 2] = v.z; iw[4 * i + 3] = v.w;
           }
         } else if constexpr (IB % 8 == 0) {
 #pragma unroll
           for (int i = 0; i < IB / 8; ++i) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(row) + i);
+            const uint2 v = reinterpret_cast<const uint2*>(row)[i];
             iw[2 * i] = v.x; iw[2 * i + 1] = v.y;
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < IB / 4; ++i) iw[i] = __ldg(reinterpret_cast<const uint32_t*>(row) + i);
+          for (int i = 0; i < IB / 4; ++i) iw[i] = reinterpret_cast<const uint32_t*>(row)[i];
         }
         if constexpr (PROD) {
-          const uint4 s4 = __ldg(reinterpret_cast<const uint4*>(a.k_sgn + (kvrow + t) * 16));
+          const uint4 s4 = *reinterpret_cast<const uint4*>(a.k_sgn + (kvrow + t) * 16);
           sg[0] = s4.x; sg[1] = s4.y; sg[2] = s4.z; sg[3] = s4.w;
         } else {
           sg[0] = sg[1] = sg[2] = sg[3] = 0u;
         }
-        if constexpr (TWO) nn = __ldg(reinterpret_cast<const uint32_t*>(a.k_nrm) + kvrow + t);
-        else nn = __ldg(a.k_nrm + kvrow + t);
-        if constexpr (HAS_V) vp = __ldg(reinterpret_cast<const uint4*>(vp_rows) + t);
+        if constexpr (TWO) nn = reinterpret_cast<const uint32_t*>(a.k_nrm)[kvrow + t];
+        else nn = a.k_nrm[kvrow + t];
+        if constexpr (HAS_V) vp = reinterpret_cast<const uint4*>(vp_rows)[t];
         else vp = make_uint4(0u, 0u, 0u, 0u);
       } else {
 #pragma unroll

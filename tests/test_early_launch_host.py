@@ -33,3 +33,10 @@ def test_no_load_that_takes_memory_for_constant(name):
 def test_every_kernel_waits(name):
     kernels = re.findall(r"__global__[^;{]*?\b(k_\w+)\s*\(", code(name))
     assert kernels and len(re.findall(r"wait_for_grid\(\);", code(name))) == len(kernels)
+
+
+def test_the_decode_reads_no_cache_row_as_constant():
+    """tq_append_decode launches the decode over the append: what it reads behind its wait was written meanwhile."""
+    text = code("decode_kernel.cuh")
+    after = text[text.index("grid_dependency_wait();"):]
+    assert "load_keys" in after and not re.search(r"__ldg\s*\(|\bload[48]\s*<", after)
