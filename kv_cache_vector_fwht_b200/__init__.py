@@ -372,6 +372,7 @@ class KVCache:
 def tq_append(q: Quantizer, cache: KVCache, k_new, v_new=None, stream=None) -> None:
     """k_new / v_new: (batch, n_kv_heads, n_tokens, d) contiguous fp32/bf16 CUDA tensors."""
     assert k_new.is_contiguous() and k_new.dim() == 4
+    assert v_new is None or (v_new.is_contiguous() and v_new.shape == k_new.shape and v_new.dtype == k_new.dtype)
     _check(_lib.tq_append(q.handle, ctypes.byref(cache.desc), _ptr(k_new), _ptr(v_new),
                           _dtype_code(k_new), k_new.shape[2], _stream(stream)), "tq_append")
 
@@ -410,6 +411,7 @@ def tq_append_decode(q: Quantizer, cache: KVCache, k_new, v_new, query, out=None
     """One decode step: tq_append(k_new, v_new) then tq_decode_attention(query), launched back
     to back (see tq.h); arguments as for the two calls."""
     assert k_new.is_contiguous() and k_new.dim() == 4
+    assert v_new is None or (v_new.is_contiguous() and v_new.shape == k_new.shape and v_new.dtype == k_new.dtype)
     assert query.is_contiguous() and query.dim() == 3
     hq = query.shape[1]
     hm = (c_int32 * hq)(*[int(v) for v in head_map]) if head_map is not None else None
