@@ -351,7 +351,9 @@ tq_status tq_norm_rope(const tq_rope* rope, int dtype, int batch, int n_tokens, 
  * statistics and outputs are held in fp32; the tensor cores cut each product off at the last bit
  * of its sum, so n tokens' products of one sign lose less than n 2^-23 of it. Non-finite cached
  * rows reach only the query rows that attend
- * to them. n_tokens = 0 is a no-op; n_q_heads * n_tokens up to 2^30.
+ * to them. n_tokens = 0 is a no-op; n_q_heads up to 512,
+ * n_q_heads * n_tokens up to 2^30. This call and those on blocks take caches of a capacity up to 2^30
+ * (else TQ_EUNSUPPORTED).
  *
  * Workspace (this call, tq_select_blocks and tq_decode_attention_blocks): zero-filled before
  * its first use, 16-byte aligned; every call leaves it reusable by any of the three, whatever
@@ -402,7 +404,7 @@ tq_status tq_select_blocks(const tq_quantizer* q, const tq_kv_cache* cache, cons
 
 /* tq_extend_attention of one token per sequence over the listed blocks alone: blocks_dev as
  * tq_select_blocks writes it; entries outside [0, n_blocks) are skipped, in any order, and an
- * entry listed twice counts twice. query / out: batch x n_q_heads x d, contiguous. */
+ * entry listed twice counts twice; n_select up to 2^30. query / out: batch x n_q_heads x d, contiguous. */
 tq_status tq_decode_attention_blocks(const tq_quantizer* q, const tq_kv_cache* cache,
                                      const void* query_dev, int q_dtype, int n_q_heads,
                                      const int32_t* head_map, float sm_scale,

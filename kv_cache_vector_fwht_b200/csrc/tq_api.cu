@@ -547,6 +547,10 @@ tq_status check_view(const tq_heads& x, int dtype, int batch, int n_heads, int n
   return TQ_OK;
 }
 
+// Positions and block numbers are counted in 32 bits, with room for a tile beyond the last: caches of up to 2^30 rows a
+// head, lists of up to 2^30 blocks.
+constexpr int kMostRows = 1 << 30;
+
 // The tables live on the device the quantizer was built on; launches go to the current one.
 tq_status check_device(const tq_quantizer* q) {
   int dev = -1;
@@ -556,7 +560,7 @@ tq_status check_device(const tq_quantizer* q) {
 
 tq_status check_heads(const tq_kv_cache* c, int n_q_heads, const int32_t* head_map) {
   if (n_q_heads <= 0 || n_q_heads > kMaxHeads) return TQ_EINVAL;
-  if (c->n_kv_heads > kMaxHeads || c->batch > 65535) return TQ_EUNSUPPORTED;
+  if (c->n_kv_heads > kMaxHeads || c->batch > 65535 || c->capacity > kMostRows) return TQ_EUNSUPPORTED;
   if (head_map) {
     for (int h = 0; h < n_q_heads; ++h)
       if (head_map[h] < 0 || head_map[h] >= c->n_kv_heads) return TQ_EINVAL;
@@ -609,6 +613,7 @@ tq_status tq_norm_rope(const tq_rope* rope, int dtype, int batch, int n_tokens, 
 tq_status tq_extend_workspace_bytes(const tq_kv_cache* c, int n_q_heads, int n_tokens, size_t* bytes) {
   if (!c || !bytes || n_q_heads <= 0 || n_tokens < 0 || c->batch <= 0 || c->n_kv_heads <= 0 || c->capacity <= 0)
     return TQ_EINVAL;
+  if (c->capacity > kMostRows || static_cast<int64_t>(n_q_heads) * n_tokens > kMostRows) return TQ_EUNSUPPORTED;
   *bytes = kWorkspaceHeader + extend_scratch_bytes(c, n_q_heads, n_tokens);
   return TQ_OK;
 }
@@ -623,7 +628,7 @@ tq_status tq_extend_attention(const tq_quantizer* q, const tq_kv_cache* c, tq_he
   if (c->value_bits == 0 || n_tokens < 0) return TQ_EINVAL;
   if (!known_dtype(q_dtype) || !known_dtype(out_dtype)) return TQ_EUNSUPPORTED;
   if (n_tokens == 0) return TQ_OK;
-  if (static_cast<int64_t>(n_q_heads) * n_tokens > (1 << 30)) return TQ_EUNSUPPORTED;   // rows are counted in 32 bits
+  if (static_cast<int64_t>(n_q_heads) * n_tokens > kMostRows) return TQ_EUNSUPPORTED;   // rows are counted in 32 bits
   if ((st = check_view(query, q_dtype, c->batch, n_q_heads, n_tokens)) != TQ_OK) return st;
   if ((st = check_view(out, out_dtype, c->batch, n_q_heads, n_tokens)) != TQ_OK) return st;
   if ((st = check_space(workspace, workspace_bytes, kWorkspaceHeader + extend_scratch_bytes(c, n_q_heads, n_tokens))) != TQ_OK)
@@ -638,7 +643,7 @@ tq_status tq_block_bounds(const tq_quantizer* q, const tq_kv_cache* c, void* bou
   tq_status st = check_cache(q, c);
   if (st != TQ_OK) return st;
   if (n_tokens < 0) return TQ_EINVAL;
-  if (c->n_kv_heads > 65535 || c->batch > 65535) return TQ_EUNSUPPORTED;
+  if (c->n_kv_heads > 65535 || c->batch > 65535 || c->capacity > kMostRows) return TQ_EUNSUPPORTED;
   if (n_tokens == 0) return TQ_OK;
   if (!bounds || !aligned16(bounds)) return TQ_EINVAL;
   if ((st = check_device(q)) != TQ_OK) return st;
@@ -648,6 +653,7 @@ tq_status tq_block_bounds(const tq_quantizer* q, const tq_kv_cache* c, void* bou
 tq_status tq_blocks_workspace_bytes(const tq_kv_cache* c, int n_q_heads, int n_select, size_t* bytes) {
   if (!c || !bytes || n_q_heads <= 0 || n_select <= 0 || c->batch <= 0 || c->n_kv_heads <= 0 || c->capacity <= 0)
     return TQ_EINVAL;
+  if (c->capacity > kMostRows || n_q_heads > kMaxHeads || n_select > kMostRows) return TQ_EUNSUPPORTED;
   *bytes = blocks_workspace(c, n_q_heads, n_select);
   return TQ_OK;
 }
@@ -661,6 +667,7 @@ tq_status tq_select_blocks(const tq_quantizer* q, const tq_kv_cache* c, const vo
   if ((st = check_heads(c, n_q_heads, head_map)) != TQ_OK) return st;
   if (!known_dtype(q_dtype)) return TQ_EUNSUPPORTED;
   if (n_select <= 0 || n_sink < 0 || n_recent < 0 || static_cast<int64_t>(n_sink) + n_recent > n_select) return TQ_EINVAL;
+  if (n_select > kMostRows) return TQ_EUNSUPPORTED;
   if (static_cast<int64_t>(c->batch) * c->n_kv_heads > kMaxCounters) return TQ_EUNSUPPORTED;
   if (!bounds || !aligned16(bounds) || !query || !aligned16(query)) return TQ_EINVAL;
   if (!blocks || (reinterpret_cast<uintptr_t>(blocks) & 3u)) return TQ_EINVAL;
@@ -678,6 +685,7 @@ tq_status tq_decode_attention_blocks(const tq_quantizer* q, const tq_kv_cache* c
   if (st != TQ_OK) return st;
   if ((st = check_heads(c, n_q_heads, head_map)) != TQ_OK) return st;
   if (c->value_bits == 0 || n_select <= 0) return TQ_EINVAL;
+  if (n_select > kMostRows) return TQ_EUNSUPPORTED;
   if (!known_dtype(q_dtype) || !known_dtype(out_dtype)) return TQ_EUNSUPPORTED;
   if (!blocks || (reinterpret_cast<uintptr_t>(blocks) & 3u)) return TQ_EINVAL;
   const int64_t row = static_cast<int64_t>(n_q_heads) * kD;
