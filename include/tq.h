@@ -298,7 +298,8 @@ tq_status tq_merge_partials(const float* parts_dev, int n_parts, int batch, int 
 /* ---------------------------------------------------- around the cache: position and norm
  * One (batch, heads, tokens, d) view of caller-owned device memory: element (b, h, t, j) at
  * data + b * stride_b + h * stride_h + t * stride_t + j (strides in elements, each of them a
- * multiple of 16 bytes; data 16-byte aligned). A fused projection's output is such a view as
+ * multiple of 16 bytes; data 16-byte aligned). Inputs may repeat rows (stride 0); the rows of an output must not
+ * overlap (strides of less than d elements are refused). A fused projection's output is such a view as
  * well as tq_append's contiguous k_new is. */
 typedef struct {
   void* data;

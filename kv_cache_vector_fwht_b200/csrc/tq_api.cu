@@ -547,6 +547,14 @@ tq_status check_view(const tq_heads& x, int dtype, int batch, int n_heads, int n
   return TQ_OK;
 }
 
+// The same of a view that is written: rows that begin less than d elements apart would lie on one another.
+tq_status check_output(const tq_heads& x, int dtype, int batch, int n_heads, int n_tokens) {
+  auto apart = [](int64_t stride) { return stride >= kD || stride <= -kD; };
+  if ((batch > 1 && !apart(x.stride_b)) || (n_heads > 1 && !apart(x.stride_h)) || (n_tokens > 1 && !apart(x.stride_t)))
+    return TQ_EINVAL;
+  return check_view(x, dtype, batch, n_heads, n_tokens);
+}
+
 // Positions and block numbers are counted in 32 bits, with room for a tile beyond the last: caches of up to 2^30 rows a
 // head, lists of up to 2^30 blocks.
 constexpr int kMostRows = 1 << 30;
@@ -603,7 +611,7 @@ tq_status tq_norm_rope(const tq_rope* rope, int dtype, int batch, int n_tokens, 
   for (int s = 0; s < 2; ++s) {
     if (heads[s] == 0) continue;
     tq_status st = check_view(src[s], dtype, batch, heads[s], n_tokens);
-    if (st == TQ_OK) st = check_view(dst[s], dtype, batch, heads[s], n_tokens);
+    if (st == TQ_OK) st = check_output(dst[s], dtype, batch, heads[s], n_tokens);
     if (st != TQ_OK) return st;
     if (w[s] && !aligned16(w[s])) return TQ_EINVAL;
   }
@@ -630,7 +638,7 @@ tq_status tq_extend_attention(const tq_quantizer* q, const tq_kv_cache* c, tq_he
   if (n_tokens == 0) return TQ_OK;
   if (static_cast<int64_t>(n_q_heads) * n_tokens > kMostRows) return TQ_EUNSUPPORTED;   // rows are counted in 32 bits
   if ((st = check_view(query, q_dtype, c->batch, n_q_heads, n_tokens)) != TQ_OK) return st;
-  if ((st = check_view(out, out_dtype, c->batch, n_q_heads, n_tokens)) != TQ_OK) return st;
+  if ((st = check_output(out, out_dtype, c->batch, n_q_heads, n_tokens)) != TQ_OK) return st;
   if ((st = check_space(workspace, workspace_bytes, kWorkspaceHeader + extend_scratch_bytes(c, n_q_heads, n_tokens))) != TQ_OK)
     return st;
   if ((st = check_device(q)) != TQ_OK) return st;

@@ -48,3 +48,29 @@ def test_rows_of_a_workspace(q):
     c, n = make_cache(), ctypes.c_size_t()
     assert lib.tq_extend_workspace_bytes(ctypes.byref(c), 4, 1 << 28, ctypes.byref(n)) == OK
     assert lib.tq_extend_workspace_bytes(ctypes.byref(c), 4, (1 << 28) + 1, ctypes.byref(n)) == EUNSUP
+
+
+@pytest.mark.parametrize("stride", [0, 64, -64, 120])
+@pytest.mark.parametrize("name", ["sb", "sh", "st"])
+def test_outputs_whose_rows_overlap(q, stride, name):
+    """Two rows on one place: which of them stays is a race. An input may repeat its rows."""
+    c = make_cache()
+    out = heads(dev(11), **{name: stride})
+    assert lib.tq_extend_attention(q.handle, ctypes.byref(c), heads(), BF16, 4, 3, 1, None, 0.0, out, BF16, dev(30), 1 << 30, None) == EINVAL
+    assert lib.tq_extend_attention(q.handle, ctypes.byref(c), heads(**{name: 0}), BF16, 4, 3, 1, None, 0.0, heads(dev(11)), BF16, dev(30),
+                                   1 << 30, None) == ECUDA
+    rope = tq.Rope(dev(1), dev(2), None, 1, 128, 0)
+    none = tq.Heads(None, 0, 0, 0)
+    assert lib.tq_norm_rope(ctypes.byref(rope), BF16, 2, 4, 128, 2, heads(), out, None, 0, none, none, None, 1, 1e-6, None) == EINVAL
+    assert lib.tq_norm_rope(ctypes.byref(rope), BF16, 2, 4, 128, 0, none, none, None, 2, heads(), out, None, 1, 1e-6, None) == EINVAL
+    assert lib.tq_norm_rope(ctypes.byref(rope), BF16, 2, 4, 128, 2, heads(**{name: 0}), heads(dev(11)), None, 0, none, none, None, 1, 1e-6,
+                            None) == ECUDA
+
+
+def test_strides_that_no_step_takes_are_free(q):
+    """One sequence, one head or one token: their stride is not used."""
+    c = make_cache(batch=1, lens=(10,))
+    out = heads(dev(11), sb=0, st=0)
+    assert lib.tq_extend_attention(q.handle, ctypes.byref(c), heads(), BF16, 4, 1, 1, None, 0.0, out, BF16, dev(30), 1 << 30, None) == ECUDA
+    assert lib.tq_extend_attention(q.handle, ctypes.byref(c), heads(), BF16, 4, 3, 1, None, 0.0, heads(dev(11), st=-512), BF16, dev(30),
+                                   1 << 30, None) == ECUDA
