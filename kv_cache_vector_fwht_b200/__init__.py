@@ -498,6 +498,12 @@ def _on_current_device(where: str, *tensors) -> int:
     return cur
 
 
+def _workspace(workspace, where: str) -> tuple[int, int]:
+    """Address and bytes of a workspace; a view with gaps holds fewer bytes than its elements reach over."""
+    _require(workspace.is_contiguous(), f"{where}: the workspace is contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _heads(x) -> Heads:
     """A (batch, heads, tokens, d) tensor with unit channel stride as the C view."""
     sb, sh, st, _ = x.stride()
@@ -602,12 +608,12 @@ def tq_extend_attention(q: Quantizer, cache: KVCache, query, out, workspace, cau
              f"{where}: query is (batch, n_q_heads, n_tokens, 128)")
     _require(out.shape == query.shape, f"{where}: out has query's shape")
     _require(query.stride(3) == 1 and out.stride(3) == 1, f"{where}: channels must be adjacent")
+    space = _workspace(workspace, where)
     device = _on_current_device(where, query, out, workspace, cache.k_idx)
     _check(_lib.tq_extend_attention(q.handle, ctypes.byref(cache.desc), _heads(query),
                                     _dtype_code(query), query.shape[1], query.shape[2], int(causal),
                                     _head_map(head_map, query.shape[1], where), sm_scale, _heads(out),
-                                    _dtype_code(out), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream, device)), where)
+                                    _dtype_code(out), *space, _stream(stream, device)), where)
 
 
 def alloc_block_bounds(cache: KVCache, device="cuda"):
@@ -661,12 +667,12 @@ def tq_select_blocks(q: Quantizer, cache: KVCache, bounds, query, blocks, worksp
     where = "tq_select_blocks"
     _check_bounds(cache, bounds, where)
     _check_step(cache, query, blocks, where)
+    space = _workspace(workspace, where)
     device = _on_current_device(where, bounds, query, blocks, workspace, cache.k_idx)
     _check(_lib.tq_select_blocks(q.handle, ctypes.byref(cache.desc), _ptr(bounds), _ptr(query),
                                  _dtype_code(query), query.shape[1],
                                  _head_map(head_map, query.shape[1], where), blocks.shape[2], n_sink,
-                                 n_recent, _ptr(blocks), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream, device)), where)
+                                 n_recent, _ptr(blocks), *space, _stream(stream, device)), where)
 
 
 def tq_decode_attention_blocks(q: Quantizer, cache: KVCache, query, blocks, out, workspace,
@@ -676,10 +682,10 @@ def tq_decode_attention_blocks(q: Quantizer, cache: KVCache, query, blocks, out,
     where = "tq_decode_attention_blocks"
     _check_step(cache, query, blocks, where)
     _require(out.shape == query.shape and out.is_contiguous(), f"{where}: out has query's shape, contiguous")
+    space = _workspace(workspace, where)
     device = _on_current_device(where, query, blocks, out, workspace, cache.k_idx)
     _check(_lib.tq_decode_attention_blocks(q.handle, ctypes.byref(cache.desc), _ptr(query),
                                            _dtype_code(query), query.shape[1],
                                            _head_map(head_map, query.shape[1], where), sm_scale,
                                            _ptr(blocks), blocks.shape[2], _ptr(out), _dtype_code(out),
-                                           _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                           _stream(stream, device)), where)
+                                           *space, _stream(stream, device)), where)
