@@ -155,6 +155,7 @@ tq_status launch_extend(const tq_quantizer* q, const tq_kv_cache* c, const tq_he
   a.counters = static_cast<int*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceHeader);
   a.err = device_error_word();
+  if (a.err == nullptr) return TQ_ECUDA;   // the kernel writes there when a wait runs out
   a.qb = query.stride_b; a.qh = query.stride_h; a.qt = query.stride_t;
   a.ob = out.stride_b; a.oh = out.stride_h; a.ot = out.stride_t;
   a.q_dtype = q_dtype;
