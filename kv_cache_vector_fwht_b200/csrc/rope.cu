@@ -256,7 +256,9 @@ tq_status launch_norm_rope(const tq_rope* r, int dtype, int batch, int n_tokens,
   // sharing a token's angles counts
   const int heads = n_heads[0] + n_heads[1];
   const int64_t pairs = (tokens + kTokens - 1) / kTokens;
-  a.chunks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((heads + 15) / 16, 148 * 8 / pairs)));
+  int device = 0;
+  cudaGetDevice(&device);
+  a.chunks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((heads + 15) / 16, sm_count(device) * 8 / pairs)));
   a.share = (heads + a.chunks - 1) / a.chunks;
   a.pos = r->pos_dev;
   a.inv_freq = r->inv_freq_dev;
