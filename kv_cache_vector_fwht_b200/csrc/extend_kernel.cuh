@@ -27,8 +27,8 @@
 // Softmax in base 2 relative to a reference per row that is raised only when a score exceeds
 // it by more than 15 (one vote a unit; then the stream's outputs in tensor memory and its sums
 // are scaled), so p <= 2^15 fits fp16. Statistics and sums in fp32. Rounded to fp16 (relative 2^-11
-// each): q', Sq' and rho, p, v; the levels are scaled by a common factor that makes them fp16
-// numbers to 2^-13 or better.
+// each): q', Sq' and rho, p, v; the levels are scaled by a common factor that brings them
+// within 2^-12.9 of fp16 numbers.
 //
 // Bounds: a long decode reads 164 bytes a token and KV head (4-bit keys and values) and spends 1240
 // thread instructions on it, most of them unpacking: 131072 tokens x 8 KV heads x 8 heads take 66 us (2.6

@@ -54,11 +54,6 @@ __device__ __forceinline__ float load_element(const void* p, int dtype, int64_t 
   const uint16_t h = static_cast<const uint16_t*>(p)[i];
   return dtype == 1 ? __uint_as_float(static_cast<uint32_t>(h) << 16) : __half2float(__ushort_as_half(h));
 }
-__device__ __forceinline__ void store_element(void* p, int dtype, int64_t i, float v) {
-  if (dtype == 0) static_cast<float*>(p)[i] = v;
-  else if (dtype == 1) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
 
 // x * s_j where bit `bit` of `word` set means s_j = -1 (a sign-bit flip, exact).
 __device__ __forceinline__ float flip_sign(float x, uint32_t word, int bit) {

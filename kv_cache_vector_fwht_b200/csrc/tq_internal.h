@@ -45,7 +45,8 @@ struct DevTables {
   // fp16 levels of the codebooks as byte pools for permute lookups (packed.cuh): the level set
   // (4-bit codes: its positive half; 2-bit: the levels themselves in lv_lo, 1-bit: the positive one
   // twice in lv_lo[0]) divided by
-  // lv_scale, a factor chosen so that every level is an fp16 number to 2^-13 or better.
+  // lv_scale, a factor chosen so that every level is within 2^-12.9 of an fp16 number (4-bit
+  // codebooks; 3-bit 2^-14.5, 2-bit 2^-15.9).
   uint32_t lv_lo[2][2], lv_hi[2][2];
   float lv_scale[2];
 };
