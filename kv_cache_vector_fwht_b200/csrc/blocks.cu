@@ -21,7 +21,7 @@ namespace {
 // results are joined. The lanes that share a word are joined at the end, by exchanges where the row's words
 // divide the warp and in shared memory otherwise.
 // Bound by instructions of the ALU pipe (lookups, minima): 8 sequences of 8192 to 32768 rows x 4
-// KV heads of 2-bit codes (36 bytes a row read, 31 MB) take 16 us, where HBM alone would take 5. With the
+// KV heads of 2-bit codes (36 bytes a row read, 31 MB) take 15 us, where HBM alone would take 5. With the
 // conversions and products of every value in fp32 it was 38.
 constexpr int kBW = 4;   // warps of a block of threads
 
