@@ -117,6 +117,10 @@ __host__ __device__ constexpr int p_bytes(int n) { return stream_rows(n) / 8 * 2
 // with two; 35 rows (N = 48) 86 and 73 us. From 64 rows on, where the softmax bounds the kernel and
 // needs 152 registers a thread, two would have 40 each and lose (a prompt's chunk 849 against 957 us).
 __host__ __device__ constexpr int unpack_groups(int n) { return n <= 48 ? 2 : 1; }
+// Stages of the raw ring that hold the tiles of group g, those j with j % groups == g: stage g, g + groups, ... A group
+// waits for its own tiles alone, so a stage never changes hands: one whose last tile was another group's may still be
+// waiting for that tile, and a wait for the next one, of the parity of the tile before it, would pass at once.
+__host__ __device__ constexpr int group_stages(int stages, int groups, int g) { return (stages + groups - 1 - g) / groups; }
 // K, V, 8 softmax, MMA, loader, and 2 warps that fill the last warpgroup
 __host__ __device__ constexpr int block_threads(int n) { return 32 * (8 * unpack_groups(n) + 12); }
 constexpr int kVBytes = kTile * kD * 2;
@@ -539,11 +543,13 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     const Levels lv0 = load_levels(a.tab, 0), lv1 = load_levels(a.tab, 1);
     const int tok = tid & 127;
     const int o_sgn = kTile * a.idx_bytes, o_nrm = o_sgn + kTile * a.sgn_bytes;
-    Ring st(warp >> 2), kb(warp >> 2);
+    const int grp = warp >> 2, own_stages = group_stages(a.stages, kG, grp);
+    Ring st(0), kb(grp);
 #pragma unroll 1
-    for (int j = warp >> 2; j < nt; j += kG, st.step(kG, a.stages), kb.step(kG, a.key_bufs)) {
-      const uint8_t* raw = sRaw + st.i * a.stage_bytes;
-      if (ok) ok = mbar_wait_ns(&ms.raw_full[st.i], st.turn, kWaitNs);
+    for (int j = grp; j < nt; j += kG, st.step(1, own_stages), kb.step(kG, a.key_bufs)) {
+      const int stage = grp + kG * st.i;
+      const uint8_t* raw = sRaw + stage * a.stage_bytes;
+      if (ok) ok = mbar_wait_ns(&ms.raw_full[stage], st.turn, kWaitNs);
       if (ok && j >= a.key_bufs) ok = mbar_wait_ns(&ms.k_empty[kb.i], kb.turn ^ 1, kWaitNs);
       tc_fence_after();
       const uint32_t tk = tlane + kb_cols * kb.i;
@@ -597,7 +603,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&ms.raw_empty[st.i]);
+        mbar_arrive(&ms.raw_empty[stage]);
         mbar_arrive(&ms.k_full[kb.i]);
       }
     }
@@ -606,11 +612,13 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     // ------------------------------------------------------------------ V: thread = token
     const int tok = tid & 127;
     const int o_vq = kTile * (a.idx_bytes + a.sgn_bytes + a.nrm_bytes), o_par = o_vq + kTile * a.vq_bytes;
-    Ring st((warp - wV) >> 2), vb((warp - wV) >> 2);
+    const int grp = (warp - wV) >> 2, own_stages = group_stages(a.stages, kG, grp);
+    Ring st(0), vb(grp);
 #pragma unroll 1
-    for (int j = (warp - wV) >> 2; j < nt; j += kG, st.step(kG, a.stages), vb.step(kG, a.value_bufs)) {
-      const uint8_t* raw = sRaw + st.i * a.stage_bytes;
-      if (ok) ok = mbar_wait_ns(&ms.raw_full[st.i], st.turn, kWaitNs);
+    for (int j = grp; j < nt; j += kG, st.step(1, own_stages), vb.step(kG, a.value_bufs)) {
+      const int stage = grp + kG * st.i;
+      const uint8_t* raw = sRaw + stage * a.stage_bytes;
+      if (ok) ok = mbar_wait_ns(&ms.raw_full[stage], st.turn, kWaitNs);
       if (ok && j >= a.value_bufs) ok = mbar_wait_ns(&ms.v_empty[vb.i], vb.turn ^ 1, kWaitNs);
       // until they have been used, the second buffer holds the rotation's matrix and the first the sketch's
       // (without the former: the second)
@@ -671,7 +679,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&ms.raw_empty[st.i]);
+        mbar_arrive(&ms.raw_empty[stage]);
         mbar_arrive(&ms.v_full[vb.i]);
       }
     }
@@ -696,11 +704,12 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     const int off = plane == 0 ? 0 : plane == 1 ? o_sgn : plane == 2 ? o_nrm : plane == 3 ? o_vq : o_par;
     const int row_bytes = a.idx_bytes + a.sgn_bytes + a.nrm_bytes + a.vq_bytes + 16;
     int j = 0;
-    Ring ring(0);
+    Ring ring(0), next(0);   // of tile j's group and, with two groups, of the other one
+    int turn_stages = group_stages(a.stages, kG, 0), next_stages = group_stages(a.stages, kG, kG - 1);
 #pragma unroll 1
-    for (; j < nt; ++j, ring.step(1, a.stages)) {
-      const int st = ring.i;
-      if (j >= a.stages) ok = mbar_wait_ns(&ms.raw_empty[st], ring.turn ^ 1, kWaitNs);
+    for (; j < nt; ++j) {
+      const int st = j % kG + kG * ring.i;
+      if (j / kG >= turn_stages) ok = mbar_wait_ns(&ms.raw_empty[st], ring.turn ^ 1, kWaitNs);
       if (!ok) break;
       int p[2], n[2];
 #pragma unroll
@@ -726,11 +735,22 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
       if (lane < 10 && mine > 0 && rb > 0)
         bulk_g2s(sRaw + st * a.stage_bytes + off + half * TQ_BLOCK * rb,
                  base + (pair * a.capacity + from) * rb, mine * rb, &ms.raw_full[st]);
+      ring.step(1, turn_stages);
+      if (kG == 2) {
+        const Ring r = ring;
+        ring = next;
+        next = r;
+        const int n = turn_stages;
+        turn_stages = next_stages;
+        next_stages = n;
+      }
     }
     // if another role gave up, wait here for the copies that nothing else will wait for
 #pragma unroll 1
-    for (int k = max(0, j - a.stages); k < j; ++k)
-      mbar_wait_ns(&ms.raw_full[k % a.stages], (k / a.stages) & 1, kWaitNs);
+    for (int k = max(0, j - kG * kMaxStages); k < j; ++k) {
+      const int grp = k % kG, n = group_stages(a.stages, kG, grp), turn = k / kG;
+      if (k + kG * n >= j) mbar_wait_ns(&ms.raw_full[grp + kG * (turn % n)], (turn / n) & 1, kWaitNs);   // the stage's last tile
+    }
     } else if (warp == wM && nt > 0) {
     // ------------------------------------------------------------------ MMA
     if (elect_one()) {
