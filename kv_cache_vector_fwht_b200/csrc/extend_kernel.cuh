@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     const Levels lv0 = load_levels(a.tab, 0), lv1 = load_levels(a.tab, 1);
     const int tok = tid & 127;
     const int o_sgn = kTile * a.idx_bytes, o_nrm = o_sgn + kTile * a.sgn_bytes;
-    const int grp = warp >> 2, own_stages = group_stages(a.stages, kG, grp);
+    const int grp = kG == 1 ? 0 : warp >> 2, own_stages = group_stages(a.stages, kG, grp);
     Ring st(0), kb(grp);
 #pragma unroll 1
     for (int j = grp; j < nt; j += kG, st.step(1, own_stages), kb.step(kG, a.key_bufs)) {
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
     // ------------------------------------------------------------------ V: thread = token
     const int tok = tid & 127;
     const int o_vq = kTile * (a.idx_bytes + a.sgn_bytes + a.nrm_bytes), o_par = o_vq + kTile * a.vq_bytes;
-    const int grp = (warp - wV) >> 2, own_stages = group_stages(a.stages, kG, grp);
+    const int grp = kG == 1 ? 0 : (warp - wV) >> 2, own_stages = group_stages(a.stages, kG, grp);
     Ring st(0), vb(grp);
 #pragma unroll 1
     for (int j = grp; j < nt; j += kG, st.step(1, own_stages), vb.step(kG, a.value_bufs)) {
