@@ -1048,8 +1048,11 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
         if (!waited && ok) ok = mbar_wait_ns(&ms.p_empty[s], (i - 1) & 1, kWaitNs);
         waited = true;
         tc_fence_after();
-        // scores that x would hold wrongly are multiplied out in tensor memory first
-        if (__any_sync(kFull, apart || sc > kLargeFactor)) {
+        // scores that x would hold wrongly are multiplied out in tensor memory first, each lane's by itself: the factors
+        // of rows past the end are anything, and must not decide how others are rounded
+        const bool out = apart || sc > kLargeFactor;
+        if (__any_sync(kFull, out)) {
+          const float mult = out ? sc : 1.f;
 #pragma unroll 1
           for (int c = 0; c < NS; c += 16) {
             uint32_t y[16];
@@ -1057,12 +1060,12 @@ __global__ void __launch_bounds__(block_threads(N), 1) k_extend(const __grid_con
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
               const float f = apart ? __uint_as_float(static_cast<uint32_t>(ms.size[r_first + c + q]) << 23) : 1.f;
-              y[q] = __float_as_uint(__uint_as_float(y[q]) * (f * sc));
+              y[q] = __float_as_uint(__uint_as_float(y[q]) * (f * mult));
             }
             tmem_st16(tS + c, y);
           }
           tmem_st_wait();
-          sc = 1.f;
+          sc = out ? 1.f : sc;
         }
         float* wmax = reinterpret_cast<float*>(myP);   // free: the last product has read it
         float* fac = ms.fac[s];

@@ -41,3 +41,26 @@ def test_the_same_bits_in_every_run(mode, bits, vbits, heads, n):
         some = q[b:b + 1, h * heads:h * heads + 1, -1:]
         ref, tol = attention64(qo, oc, some.float().cpu().numpy(), [[length]], vbits)
         check(outs[0][b:b + 1, h * heads:h * heads + 1, -1:], ref, tol, F32)
+
+
+@pytest.mark.parametrize("mode,bits,vbits", [("prod", 3, 4), ("mse", 2, 2), ("grouped", 2, 4)])
+@pytest.mark.parametrize("heads,n", [(5, 1), (3, 20), (8, 12)])
+@pytest.mark.parametrize("length", [3, 71, 143])
+def test_rows_behind_the_end_change_no_bit(mode, bits, vbits, heads, n, length):
+    """Zeros, the largest norms, NaN or another sequence's rows behind the end: the outputs are the same, to the bit."""
+    require_cuda()
+    qo, qg = quantizers(mode, bits)
+    cache = tq.KVCache(qg, 1, 1, 160, value_bits=vbits, device="cuda:0")
+    g = torch.Generator("cuda").manual_seed(length)
+    k, v = (torch.randn(1, 1, length, 128, generator=g, device="cuda").to(BF16) for _ in range(2))
+    tq.tq_append(qg, cache, k, v)
+    q = 3 * torch.randn(1, heads, n, 128, generator=g, device="cuda")
+    ws, outs = tq.alloc_extend_workspace(cache, heads, n), []
+    for junk in (0, 0x7bff, 0x7bff - (1 << 11), -1, 0x3c00):
+        cache.k_norms[length:] = junk
+        cache.v_params[length:] = junk
+        cache.k_idx[length:] = junk & 255
+        outs.append(torch.empty(q.shape, dtype=F32, device="cuda"))
+        tq.tq_extend_attention(qg, cache, q, outs[-1], ws)
+    tq.tq_sync_status()
+    assert outs[0].isfinite().all() and all(torch.equal(outs[0], o) for o in outs[1:])
