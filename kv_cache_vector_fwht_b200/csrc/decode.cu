@@ -163,7 +163,7 @@ tq_status plan_decode(const tq_quantizer* q, const tq_kv_cache* c, int n_q_heads
   double best_cost = 1e300;
   const int max_try = std::max(1, std::min(cap_splits, (max_len + 255) / 256));
   for (int s = 1; s <= max_try; ++s) {
-    const int tps = ((max_len + s - 1) / s + 31) & ~31;
+    const int tps = std::max(32, ((max_len + s - 1) / s + 31) & ~31);   // all sequences empty: one split of nothing
     if ((max_len + tps - 1) / tps != s) continue;
     const double waves = std::ceil(static_cast<double>(pairs) * s / sms);
     const double cost = waves * (tps + chunk) + (s > 1 ? 8.0 * s : 0.0);
