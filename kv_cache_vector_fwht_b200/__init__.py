@@ -256,7 +256,7 @@ class Quantizer:
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
-        if h:
+        if h and _lib is not None:   # at the interpreter's end the module's names may be gone
             _lib.tq_free(h)
 
     def alloc_key_planes(self, n_rows: int, device="cuda"):

@@ -31,10 +31,10 @@
 // within 2^-12.9 of fp16 numbers.
 //
 // Bounds: a long decode reads 164 bytes a token and KV head (4-bit keys and values) and spends 1240
-// thread instructions on it, most of them unpacking: 131072 tokens x 8 KV heads x 8 heads take 67 us (2.6
-// TB/s), issue slots 62 % and ALU pipe 59 % busy. A chunk of a prompt (128 rows) is bound by the softmax's
-// instructions: 2048 tokens over 16384, 28/4 heads, take 772 us (0.58 PFLOP/s of products, mask counted
-// out), issue slots 56 %, tensor pipe 31 %. One short token (333 cached) takes 9.8 us, nearly all latency.
+// thread instructions on it, most of them unpacking: 131072 tokens x 8 KV heads x 8 heads take 68 us (2.5
+// TB/s), issue slots 62 % and ALU pipe 58 % busy. A chunk of a prompt (128 rows) is bound by the softmax's
+// instructions: 2048 tokens over 16384, 28/4 heads, take 780 us (0.58 PFLOP/s of products, mask counted
+// out), issue slots 55 %, tensor pipe 30 %. One short token (333 cached) takes 9.8 us, nearly all latency.
 #pragma once
 
 #include <cmath>
